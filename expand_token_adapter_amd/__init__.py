@@ -10,9 +10,19 @@ device memory and streams.
     v = lora_shrink(x, table, seg)                       # v = A_a x    (fp32)
     lora_expand_add(v, table, seg, y)                    # y += s_a B_a v
     lora_backward(x_ft, dy, table, grads, seg_ft, dx)    # dX, dA, dB  (+=)
+
+Rows and frozen weights in 8 bits (e4m3 codes, one power-of-two scale per
+block of 128):
+
+    xq = lora_quant_rows(x)                              # save the layer input
+    wq, wt = lora_quant_weight(W), lora_quant_weight(W, transpose=True)
+    y = lora_base_product(xq, wq)                        # y = W x
+    lora_base_product(lora_quant_rows(dy), wt, y=dx)     # dX = W^T dY
+    lora_backward_quant(xq[s:e], dy, table, grads, seg_ft, dx)   # dX, dA, dB from the saved rows
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -22,13 +32,14 @@ from . import _abi
 from ._abi import LORA_BF16, LORA_F32, LORA_MAX_RANK, LoraError
 
 __all__ = [
-    "AdapterTable", "GradTable", "Segments", "LoraError",
+    "AdapterTable", "GradTable", "QuantRows", "QuantWeight", "Segments", "LoraError",
     "lora_segments_build", "lora_segments_build_batch", "lora_shrink", "lora_shrink_noalloc", "lora_expand_add",
     "lora_forward",
     "lora_forward_multi", "lora_backward", "lora_backward_preemptible", "lora_adamw_step",
+    "lora_quant_rows", "lora_dequant_rows", "lora_quant_weight", "lora_base_product", "lora_backward_quant",
     "lora_abi_version", "lora_status_string",
     "lora_segments_workspace_bytes", "lora_shrink_workspace_bytes", "lora_backward_workspace_bytes",
-    "lora_segments_sched_elems",
+    "lora_segments_sched_elems", "lora_base_product_workspace_bytes", "lora_backward_quant_workspace_bytes",
 ]
 
 _DTYPES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
@@ -205,6 +216,71 @@ class GradTable:
     @property
     def ptr(self) -> int:
         return self.table.data_ptr()
+
+
+class _Quant:
+    """8-bit floating point matrix: value = code * 2^(scale - 127), one scale per block of 128.
+
+    codes: uint8 (or float8_e4m3fn) [rows, ld], scales: uint8 [.., lds], on one GPU with contiguous
+    rows; ld a multiple of 128 and lds of 4 (widths rounded up to these).  The codes of columns from the last value's to
+    the end of its block of 128 are zeros."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, scale_rows: int, cols: int):
+        if codes.dtype not in (torch.uint8, torch.float8_e4m3fn) or scales.dtype != torch.uint8:
+            raise TypeError("codes must be uint8 or float8_e4m3fn, scales uint8")
+        _on_gpu(codes, scales)
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must live on one device")
+        block = _abi.LORA_QUANT_BLOCK
+        for name, t, r, c, unit in (("codes", codes, rows, -(-cols // block) * block, block),
+                                    ("scales", scales, scale_rows, -(-cols // (4 * block)) * 4, 4)):
+            if t.dim() != 2 or t.stride(1) != 1 or t.shape[0] != r or t.shape[1] < c:
+                raise ValueError(f"{name} must be [{r}, >= {c}] with contiguous rows")
+            if r > 1 and (t.stride(0) % unit or t.stride(0) < t.shape[1]) or r == 1 and t.shape[1] % unit:
+                raise ValueError(f"the row pitch of {name} must be a multiple of {unit}")
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        self.c = _abi.LoraQuant(codes.data_ptr(), codes.stride(0) if rows > 1 else codes.shape[1],
+                                scales.data_ptr(), scales.stride(0) if scale_rows > 1 else scales.shape[1])
+
+    @staticmethod
+    def _buffers(rows: int, scale_rows: int, cols: int, device):
+        block = _abi.LORA_QUANT_BLOCK
+        nb = -(-cols // block)
+        u8 = dict(dtype=torch.uint8, device=device)
+        return (torch.empty(rows, nb * block, **u8), torch.full((scale_rows, -(-nb // 4) * 4), 127, **u8))
+
+
+class QuantRows(_Quant):
+    """Rows (activations) in 8 bits: codes [T, >= round_up(d, 128)], scales [T, >= round_up(ceil(d / 128), 4)].
+
+    A slice of rows (q[a:b]) is a QuantRows over the same memory."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, d: int):
+        T = int(codes.shape[0])
+        super().__init__(codes, scales, T, T, d)
+        self.T, self.d = T, int(d)
+
+    @classmethod
+    def empty(cls, T: int, d: int, device) -> "QuantRows":
+        """Buffers for T rows of d values, contents unset (a checkpoint is filled piece by piece)."""
+        return cls(*cls._buffers(T, T, d, device), d)
+
+    def __len__(self) -> int:
+        return self.T
+
+    def __getitem__(self, rows: slice) -> "QuantRows":
+        if not isinstance(rows, slice) or rows.step not in (None, 1):
+            raise TypeError("rows are taken as a slice of consecutive rows")
+        return QuantRows(self.codes[rows], self.scales[rows], self.d)
+
+
+class QuantWeight(_Quant):
+    """A weight [d_out, d_in] in 8 bits, 128 x 128 values per scale: codes [d_out, >= round_up(d_in, 128)],
+    scales [ceil(d_out / 128), >= round_up(ceil(d_in / 128), 4)]."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, d_out: int, d_in: int):
+        super().__init__(codes, scales, d_out, -(-d_out // _abi.LORA_QUANT_BLOCK), d_in)
+        self.d_out, self.d_in = int(d_out), int(d_in)
 
 
 class Segments:
@@ -414,24 +490,47 @@ def lora_backward_preemptible(x: torch.Tensor, dy: torch.Tensor, adapters: Adapt
               (grant_ptr, status.data_ptr()))
 
 
+def lora_backward_quant(x: QuantRows, dy: torch.Tensor, adapters: AdapterTable, grads: GradTable, seg_ft: Segments,
+                        dx: Optional[torch.Tensor] = None, v_saved: Optional[torch.Tensor] = None,
+                        r_max: Optional[int] = None, ws: Optional[torch.Tensor] = None) -> None:
+    """lora_backward from the fine-tuning rows' saved 8-bit layer input, read as it is.
+
+    dX, dA and dB (+=) equal those of lora_backward on lora_dequant_rows(x) bit for bit."""
+    if not isinstance(x, QuantRows):
+        raise TypeError("x must be a QuantRows (lora_quant_rows)")
+    _backward("lora_backward_quant", x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, ())
+
+
 def _backward(fn, x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, extra) -> None:
-    _on_gpu(x, dy, dx, v_saved)
-    px, T, d_in, ldx = _rows(x, "x")
+    quant = isinstance(x, QuantRows)
+    if quant:
+        T, d_in, rows = x.T, x.d, (x.c,)
+        if x.device != adapters.device:
+            raise ValueError(f"{fn}: x and the adapters are on different devices")
+        if d_in != adapters.d_in:
+            raise ValueError(f"{fn}: x has {d_in} columns, the adapters' d_in is {adapters.d_in}")
+    else:
+        _on_gpu(x)
+        px, T, d_in, ldx = _rows(x, "x")
+        rows = (px, ldx)
+    _on_gpu(dy, dx, v_saved)
     pdy, Td, d_out, lddy = _rows(dy, "dy")
     if Td != T:
         raise ValueError("x and dy must have the same number of rows")
     pdx, lddx = 0, 0
     if dx is not None:
         pdx, Tx, _, lddx = _rows(dx, "dx")
-        if Tx != T or dx.dtype != x.dtype:
+        if Tx != T or dx.dtype != (adapters.dtype if quant else x.dtype):
             raise ValueError("dx must match x")
+        if quant and (dx.shape[1] != d_in or dx.device != adapters.device):
+            raise ValueError(f"{fn}: dx must have {d_in} columns on the adapters' device")
     pvs, ldv = 0, 0
     if v_saved is not None:
         pvs, _, _, ldv = _rows(v_saved, "v_saved")
     if len(grads.dA) != len(adapters):
         raise ValueError("the gradient table must have one entry per adapter")
     r_max = adapters.r_max if r_max is None else r_max
-    _check_batch(fn, adapters, seg_ft, T, x=x, v=v_saved, r_max=r_max)
+    _check_batch(fn, adapters, seg_ft, T, x=None if quant else x, v=v_saved, r_max=r_max)
     if dy.dtype != adapters.dtype or dy.shape[1] != adapters.d_out or dy.device != adapters.device:
         raise ValueError(f"{fn}: dy must be {adapters.dtype} with d_out = {adapters.d_out} columns on the adapters' device")
     for i, (ga, gb) in enumerate(zip(grads.dA, grads.dB)):
@@ -442,13 +541,106 @@ def _backward(fn, x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, extra)
         if ga.device != adapters.device or gb.device != adapters.device:
             raise ValueError(f"{fn}: gradient entry {i} is on another device")
     lib = _abi.load()
+    code = _dtype_code(dy if quant else x)
     if ws is None:  # a caller's workspace is size-checked by the library (LORA_ERR_WORKSPACE)
-        ws = torch.empty(max(lib.lora_backward_workspace_bytes(_dtype_code(x), T, d_in, d_out, r_max), 1),
+        ws = torch.empty(max(lib.lora_backward_workspace_bytes(code, T, d_in, d_out, r_max), 1),
                          dtype=torch.uint8, device=x.device)
-    st = getattr(lib, fn)(_dtype_code(x), px, ldx, pdy, lddy, pdx or None, lddx, T, d_in, d_out, adapters.ptr,
-                          grads.ptr, len(adapters), r_max, seg_ft.c, pvs or None, ldv, ws.data_ptr(), ws.numel(),
-                          *extra, _stream(x.device))
+    with _on_device(x.device):
+        st = getattr(lib, fn)(code, *rows, pdy, lddy, pdx or None, lddx, T, d_in, d_out, adapters.ptr,
+                              grads.ptr, len(adapters), r_max, seg_ft.c, pvs or None, ldv, ws.data_ptr(), ws.numel(),
+                              *extra, _stream(x.device))
     _abi.check(fn, st)
+
+
+def _on_device(dev: torch.device):
+    """Makes dev the current device where it is not (kernels are launched on the current device)."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def lora_quant_rows(x: torch.Tensor, out: Optional[QuantRows] = None) -> QuantRows:
+    """Save rows x [T, d] (bfloat16 or float32) in 8 bits; out: buffers to fill (QuantRows.empty, or a slice)."""
+    _on_gpu(x)
+    code = _dtype_code(x)
+    px, T, d, ldx = _rows(x, "x")
+    if out is None:
+        out = QuantRows.empty(T, d, x.device)
+    elif out.T != T or out.d != d or out.device != x.device:
+        raise ValueError(f"out must hold {T} rows of {d} values on x's device")
+    with _on_device(x.device):
+        st = _abi.load().lora_quant_rows(code, px, ldx, T, d, out.c, _stream(x.device))
+    _abi.check("lora_quant_rows", st)
+    return out
+
+
+def lora_dequant_rows(q: QuantRows, dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The rows that q holds, as a tensor [T, d] of dtype (or into out, whose type counts)."""
+    if out is None:
+        out = torch.empty(q.T, q.d, dtype=dtype, device=q.device)
+    _on_gpu(out)
+    code = _dtype_code(out)
+    px, T, d, ldx = _rows(out, "out")
+    if T != q.T or d != q.d or out.device != q.device:
+        raise ValueError(f"out must be [{q.T}, {q.d}] on q's device")
+    with _on_device(q.device):
+        st = _abi.load().lora_dequant_rows(code, q.c, T, d, px, ldx, _stream(q.device))
+    _abi.check("lora_dequant_rows", st)
+    return out
+
+
+def lora_quant_weight(w: torch.Tensor, transpose: bool = False, out: Optional[QuantWeight] = None) -> QuantWeight:
+    """A frozen weight [d_out, d_in] (bfloat16 or float32) in 8 bits; transpose: the form of its transpose."""
+    _on_gpu(w)
+    code = _dtype_code(w)
+    pw, d_out, d_in, ldw = _rows(w, "w")
+    rows, cols = (d_in, d_out) if transpose else (d_out, d_in)
+    if out is None:
+        out = QuantWeight(*QuantWeight._buffers(rows, -(-rows // _abi.LORA_QUANT_BLOCK), cols, w.device), rows, cols)
+    elif out.d_out != rows or out.d_in != cols or out.device != w.device:
+        raise ValueError(f"out must be a [{rows}, {cols}] weight on w's device")
+    with _on_device(w.device):
+        st = _abi.load().lora_quant_weight(code, pw, ldw, d_out, d_in, int(bool(transpose)), out.c, _stream(w.device))
+    _abi.check("lora_quant_weight", st)
+    return out
+
+
+def lora_base_product_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
+    return _abi.load().lora_base_product_workspace_bytes(T, d_in, d_out)
+
+
+def lora_base_product(x: QuantRows, w: QuantWeight, y: Optional[torch.Tensor] = None, accumulate: bool = False,
+                      dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = W x for every row (accumulate: y += W x); without y, a new tensor [T, d_out] of dtype."""
+    if not isinstance(x, QuantRows) or not isinstance(w, QuantWeight):
+        raise TypeError("x must be a QuantRows and w a QuantWeight")
+    if x.d != w.d_in or x.device != w.device:
+        raise ValueError(f"x has {x.d} columns on {x.device}, w has d_in = {w.d_in} on {w.device}")
+    dev = x.device
+    if y is None:
+        if accumulate:
+            raise ValueError("accumulate needs y")
+        y = torch.empty(x.T, w.d_out, dtype=dtype, device=dev)
+    _on_gpu(y)
+    code = _dtype_code(y)
+    py, T, d_out, ldy = _rows(y, "y")
+    if T != x.T or d_out != w.d_out or y.device != dev:
+        raise ValueError(f"y must be [{x.T}, {w.d_out}] on x's device")
+    lib = _abi.load()
+    if ws is None:  # a caller's workspace is size-checked by the library (LORA_ERR_WORKSPACE)
+        ws = torch.empty(max(lib.lora_base_product_workspace_bytes(T, x.d, d_out), 1), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous on x's device")
+    with _on_device(dev):
+        st = lib.lora_base_product(code, x.c, T, x.d, w.c, d_out, py, ldy, int(bool(accumulate)), ws.data_ptr(),
+                                   ws.numel() * ws.element_size(), _stream(dev))
+    _abi.check("lora_base_product", st)
+    return y
+
+
+def lora_backward_quant_workspace_bytes(dtype: torch.dtype, T_ft: int, d_in: int, d_out: int, r_max: int) -> int:
+    return _abi.load().lora_backward_quant_workspace_bytes(_DTYPES[dtype], T_ft, d_in, d_out, r_max)
 
 
 def lora_adamw_step(tensors, *, step: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,

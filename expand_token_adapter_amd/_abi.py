@@ -65,6 +65,13 @@ class LoraSlice(ctypes.Structure):
 LORA_MAX_SLICES = 3
 
 
+LORA_QUANT_BLOCK = 128
+
+
+class LoraQuant(ctypes.Structure):
+    _fields_ = [("codes", _vp), ("ld", _i64), ("scales", _vp), ("lds", _i64)]
+
+
 class LoraSegmentsJob(ctypes.Structure):
     _fields_ = [("adapter_ids", _vp), ("T", _i32), ("seg", LoraSegments), ("ws", _vp), ("ws_bytes", _sz)]
 
@@ -94,6 +101,15 @@ SIGNATURES = {
     "lora_backward_preemptible": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _i32,
                                                  _vp, _vp, _i32, _i32, LoraSegments, _vp, _i64, _vp, _sz, _vp, _vp,
                                                  _vp]),
+    "lora_quant_rows": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _i32, LoraQuant, _vp]),
+    "lora_dequant_rows": (ctypes.c_int, [ctypes.c_int, LoraQuant, _i32, _i32, _vp, _i64, _vp]),
+    "lora_quant_weight": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _i32, _i32, LoraQuant, _vp]),
+    "lora_base_product_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "lora_base_product": (ctypes.c_int, [ctypes.c_int, LoraQuant, _i32, _i32, LoraQuant, _i32, _vp, _i64, _i32, _vp,
+                                         _sz, _vp]),
+    "lora_backward_quant_workspace_bytes": (_sz, [ctypes.c_int, _i32, _i32, _i32, _i32]),
+    "lora_backward_quant": (ctypes.c_int, [ctypes.c_int, LoraQuant, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
+                                           _i32, _i32, LoraSegments, _vp, _i64, _vp, _sz, _vp]),
 }
 
 _lib = None

@@ -91,30 +91,39 @@ namespace {
 // contract_fixup_kernel in the next launch.  The contraction and the expand
 // use one LDS buffer (a workgroup runs one of them).
 // (fp32: one workgroup per CU by its LDS, so no register limit for more)
-template <int DT, int KS, bool NT>
+template <int DT, int KS, bool NT, bool XQ>
 __global__ __launch_bounds__(4 * kWave) __attribute__((amdgpu_waves_per_eu(DT == LORA_F32 ? 1 : (KS == 4 ? 2 : 3))))
 void xside_kernel(ContractParams cp, int n_ctr, ExpandParams ep, int n_expand, DyParams dp) {
     constexpr int kC = ContractLds<DT, 4>::kBytes, kE = ExpandLds<KS>::kBytes;
     __shared__ __attribute__((aligned(16))) char s_lds[kC > kE ? kC : kE];
     const int b = (int)blockIdx.x;
     if (b < n_ctr)
-        contract_body<DT, NT, 4>(cp, b, n_ctr, s_lds);
+        contract_body<DT, NT, 4, XQ>(cp, b, n_ctr, s_lds);
     else if (b < n_ctr + n_expand)
         expand_body<DT, true, KS>(ep, b - n_ctr, n_expand, s_lds);
     else
         dy_fixup_body(dp, b - n_ctr - n_expand);
 }
 
+template <int DT, bool NT, bool XQ>
+void launch_xside_q(int ks, const ContractParams& cp, const ExpandParams& ep, const DyParams& dp, unsigned n_expand,
+                    unsigned n_dy, hipStream_t st) {
+    const dim3 grid(kXsideCtrGrid + n_expand + n_dy), block(4 * kWave);
+    if (ks == 1)
+        hipLaunchKernelGGL((xside_kernel<DT, 1, NT, XQ>), grid, block, 0, st, cp, kXsideCtrGrid, ep, (int)n_expand, dp);
+    else if (ks == 2)
+        hipLaunchKernelGGL((xside_kernel<DT, 2, NT, XQ>), grid, block, 0, st, cp, kXsideCtrGrid, ep, (int)n_expand, dp);
+    else
+        hipLaunchKernelGGL((xside_kernel<DT, 4, NT, XQ>), grid, block, 0, st, cp, kXsideCtrGrid, ep, (int)n_expand, dp);
+}
+
 template <int DT, bool NT>
 void launch_xside(int ks, const ContractParams& cp, const ExpandParams& ep, const DyParams& dp, unsigned n_expand,
                   unsigned n_dy, hipStream_t st) {
-    const dim3 grid(kXsideCtrGrid + n_expand + n_dy), block(4 * kWave);
-    if (ks == 1)
-        hipLaunchKernelGGL((xside_kernel<DT, 1, NT>), grid, block, 0, st, cp, kXsideCtrGrid, ep, (int)n_expand, dp);
-    else if (ks == 2)
-        hipLaunchKernelGGL((xside_kernel<DT, 2, NT>), grid, block, 0, st, cp, kXsideCtrGrid, ep, (int)n_expand, dp);
+    if (cp.xs)
+        launch_xside_q<DT, NT, true>(ks, cp, ep, dp, n_expand, n_dy, st);
     else
-        hipLaunchKernelGGL((xside_kernel<DT, 4, NT>), grid, block, 0, st, cp, kXsideCtrGrid, ep, (int)n_expand, dp);
+        launch_xside_q<DT, NT, false>(ks, cp, ep, dp, n_expand, n_dy, st);
 }
 }  // namespace
 
@@ -151,7 +160,8 @@ bool use_stream_path(int dtype, int32_t T, int64_t lddy, int32_t d_in, int32_t d
            (int64_t)BwdWs::dy_slices(d_out) * T * 64 < lim && (!v_saved || (int64_t)T * ldv * 4 < lim);
 }
 
-int backward_impl(int dtype, const void* x, int64_t ldx, const void* dy, int64_t lddy, void* dx, int64_t lddx,
+// xq: saved 8-bit rows in place of x (null: x, ldx).
+int backward_impl(int dtype, const void* x, int64_t ldx, const lora_quant* xq, const void* dy, int64_t lddy, void* dx, int64_t lddx,
                   int32_t T_ft, int32_t d_in, int32_t d_out, const lora_adapter* adapters,
                   const lora_adapter_grad* grads, int32_t num_adapters, int32_t r_max, lora_segments seg_ft,
                   const float* v_saved, int64_t ldv, void* ws, size_t ws_bytes, const int32_t* grant,
@@ -160,7 +170,7 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const void* dy, int64_t
     if (rc != LORA_OK) return rc;
     if (d_in < 1 || d_out < 1 || !grads || ((uintptr_t)grads & 7u)) return LORA_ERR_INVALID_ARG;
     if (T_ft == 0) return LORA_OK;
-    if ((rc = check_matrix(x, d_in, ldx)) != LORA_OK) return rc;
+    if ((rc = xq ? check_quant(*xq, d_in) : check_matrix(x, d_in, ldx)) != LORA_OK) return rc;
     if ((rc = check_matrix(dy, d_out, lddy)) != LORA_OK) return rc;
     if (dx && (rc = check_matrix(dx, d_in, lddx)) != LORA_OK) return rc;
     if (v_saved && (rc = check_f32_rows(v_saved, ldv, r_max)) != LORA_OK) return rc;
@@ -215,8 +225,10 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const void* dy, int64_t
     // one-pass kernel, rank-major for the contraction.
     if (!v_saved) {
         ShrinkParams vp = sp;
-        vp.x = x;
-        vp.ldx = ldx;
+        vp.x = xq ? xq->codes : x;
+        vp.ldx = xq ? xq->ld : ldx;
+        vp.xs = xq ? xq->scales : nullptr;
+        vp.ldxs = xq ? xq->lds : 0;
         vp.K = d_in;
         vp.nslices = shrink_slices(dtype, d_in);
         ReduceParams vr = rp;
@@ -291,8 +303,10 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const void* dy, int64_t
 
     // dA += s g^T x (and, on the two-pass path, dB += s dy^T v).
     ContractParams cp{};
-    cp.x = x;
-    cp.ldx = ldx;
+    cp.x = xq ? xq->codes : x;
+    cp.ldx = xq ? xq->ld : ldx;
+    cp.xs = xq ? xq->scales : nullptr;
+    cp.ldxs = xq ? xq->lds : 0;
     cp.dy = dy;
     cp.lddy = lddy;
     cp.gT = gT;
@@ -354,7 +368,7 @@ extern "C" int lora_backward(int dtype, const void* x, int64_t ldx, const void* 
                              const lora_adapter_grad* grads, int32_t num_adapters, int32_t r_max,
                              lora_segments seg_ft, const float* v_saved, int64_t ldv, void* ws, size_t ws_bytes,
                              void* stream) {
-    return backward_impl(dtype, x, ldx, dy, lddy, dx, lddx, T_ft, d_in, d_out, adapters, grads, num_adapters, r_max,
+    return backward_impl(dtype, x, ldx, nullptr, dy, lddy, dx, lddx, T_ft, d_in, d_out, adapters, grads, num_adapters, r_max,
                          seg_ft, v_saved, ldv, ws, ws_bytes, nullptr, nullptr, stream);
 }
 
@@ -365,6 +379,20 @@ extern "C" int lora_backward_preemptible(int dtype, const void* x, int64_t ldx, 
                                          const float* v_saved, int64_t ldv, void* ws, size_t ws_bytes,
                                          const int32_t* grant, int32_t* status, void* stream) {
     if (!grant || !status || ((uintptr_t)grant & 3u) || ((uintptr_t)status & 3u)) return LORA_ERR_INVALID_ARG;
-    return backward_impl(dtype, x, ldx, dy, lddy, dx, lddx, T_ft, d_in, d_out, adapters, grads, num_adapters, r_max,
+    return backward_impl(dtype, x, ldx, nullptr, dy, lddy, dx, lddx, T_ft, d_in, d_out, adapters, grads, num_adapters, r_max,
                          seg_ft, v_saved, ldv, ws, ws_bytes, grant, status, stream);
+}
+
+extern "C" size_t lora_backward_quant_workspace_bytes(int dtype, int32_t T_ft, int32_t d_in, int32_t d_out,
+                                                      int32_t r_max) {
+    return lora_backward_workspace_bytes(dtype, T_ft, d_in, d_out, r_max);
+}
+
+extern "C" int lora_backward_quant(int dtype, lora_quant x, const void* dy, int64_t lddy, void* dx, int64_t lddx,
+                                   int32_t T_ft, int32_t d_in, int32_t d_out, const lora_adapter* adapters,
+                                   const lora_adapter_grad* grads, int32_t num_adapters, int32_t r_max,
+                                   lora_segments seg_ft, const float* v_saved, int64_t ldv, void* ws, size_t ws_bytes,
+                                   void* stream) {
+    return backward_impl(dtype, nullptr, 0, &x, dy, lddy, dx, lddx, T_ft, d_in, d_out, adapters, grads, num_adapters,
+                         r_max, seg_ft, v_saved, ldv, ws, ws_bytes, nullptr, nullptr, stream);
 }

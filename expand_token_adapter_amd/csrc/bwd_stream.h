@@ -64,25 +64,7 @@ constexpr int kDyCols = 256;                  // d_out columns per slice
 constexpr int kDyFixFloats = kDyCols * 16;    // a cut pair's partial dB tile
 static_assert(kStWaves * kStTileBytes >= kStWaves * (kDyCols / 16) * kWave * 16, "the dB sums reuse a buffer's tiles");
 
-// A buffer load of `bytes` (4 or 16) per lane straight into LDS: lane L's
-// bytes land at lds + bytes * L (lds wave-uniform); bytes past the buffer
-// (voff) are not fetched.  soff (wave-uniform) adds to the memory address
-// only.  Issued from assembly: the compiler does not track it, so the caller
-// waits (vmcnt) before any read of those LDS bytes and before reusing them.
-__device__ __forceinline__ void dma_lds(buf_rsrc_t r, uint32_t voff, uint32_t soff, void* lds, int bytes) {
-    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-    if (bytes == 16)
-        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                     :
-                     : "s"(m0), "v"(voff), "s"(r), "s"(soff)
-                     : "memory", "m0");
-    else
-        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                     :
-                     : "s"(m0), "v"(voff), "s"(r), "s"(soff)
-                     : "memory", "m0");
-}
-// The same for 16 bytes with the nontemporal hint: dY is read once, and its
+// dma_lds of 16 bytes with the nontemporal hint: dY is read once, and its
 // stream then leaves in L2 the g partials, cut dB tiles, B_a and v that the
 // next kernels re-read (mixed batch: backward 52.2 against 55.3 us).
 __device__ __forceinline__ void dma_lds16_nt(buf_rsrc_t r, uint32_t voff, uint32_t soff, void* lds) {

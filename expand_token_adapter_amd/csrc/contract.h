@@ -7,7 +7,10 @@
 // order, so results are bit-reproducible.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
+#include "quant.h"
 
 namespace lora {
 
@@ -30,6 +33,9 @@ __device__ __forceinline__ int rotated(int kc0, int n, int rot, int i) {
 // 64 columns per wave and step) become MFMA B operands through LDS: bf16
 // tiles are stored as loaded and read back transposed with
 // ds_read_b64_tr_b16; fp32 tiles are written transposed element by element.
+// x may come as saved 8-bit rows: a lane then loads the 8 codes of its row and
+// columns and their scale byte, and decodes them where it writes the tile, so
+// the loads stay as far ahead as the others.
 // g and v come rank-major ([k][sorted position]) from the shrink kernel.
 //
 // Work split ("stream-K"): the work is the list of (tile, 32-row window)
@@ -51,8 +57,10 @@ constexpr int kCtPitch = 32 + 8;  // fp32 path: LDS pitch (elements) of a transp
 constexpr int kQPitch = 64 + 8;   // bf16 path: LDS pitch (elements) of a staged row
 
 struct ContractParams {
-    const void* x;
+    const void* x;    // or, for saved 8-bit rows, their codes
     int64_t ldx;
+    const uint8_t* xs;  // scales of saved 8-bit rows
+    int64_t ldxs;
     const void* dy;
     int64_t lddy;
     const float* gT;  // [r_max][ldT] by sorted position
@@ -123,11 +131,11 @@ struct ContractLds {
     static constexpr int kBytes = kTransBytes > kRedBytes ? kTransBytes : kRedBytes;
 };
 
-// Raw loads of one 32-row window: this lane's 4 rows x 8 columns of Q and,
-// per rank block, 8 positions of P.
-template <int DT>
+// Raw loads of one 32-row window: this lane's 4 rows x 8 columns of Q (Q8:
+// saved 8-bit rows) and, per rank block, 8 positions of P.
+template <int DT, bool Q8>
 struct ContractWin {
-    Frag<DT> q[4];
+    std::conditional_t<Q8, QuantRaw, Frag<DT>> q[4];
     f32x4_t pv[kContractMB][2];
 };
 
@@ -142,12 +150,16 @@ __device__ __forceinline__ void contract_rows(int32_t* rows, const int32_t* perm
 }
 
 // NT: the window's x / dY rows are loaded with the nontemporal hint.
-template <int DT, bool NT>
-__device__ __forceinline__ void contract_load(ContractWin<DT>& W, const char* q, int64_t ldq, const float* PT,
-                                              int64_t ldT, const int32_t* rows, int win, int c0, int lcol, int rank0,
-                                              int r, int lane) {
+template <int DT, bool NT, bool Q8>
+__device__ __forceinline__ void contract_load(ContractWin<DT, Q8>& W, const char* q, int64_t ldq, const uint8_t* qs,
+                                              int64_t ldqs, const float* PT, int64_t ldT, const int32_t* rows, int win,
+                                              int c0, int lcol, int rank0, int r, int lane) {
     constexpr int EB = Frag<DT>::kBytes;
-    if constexpr (NT && DT == LORA_BF16) {
+    if constexpr (Q8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            W.q[j] = QuantRaw::load(reinterpret_cast<const uint8_t*>(q) + rows[j] * ldq, qs + rows[j] * ldqs, c0 + lcol);
+    } else if constexpr (NT && DT == LORA_BF16) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             W.q[j].q = __builtin_nontemporal_load(
@@ -166,18 +178,26 @@ __device__ __forceinline__ void contract_load(ContractWin<DT>& W, const char* q,
     }
 }
 
-template <int DT>
-__device__ __forceinline__ void contract_compute(const ContractWin<DT>& W, char* tile, f32x4_t (*acc)[4], int win,
+template <int DT, bool Q8>
+__device__ __forceinline__ void contract_compute(const ContractWin<DT, Q8>& W, char* tile, f32x4_t (*acc)[4], int win,
                                                  int lo, int hi, int lcol, int lrow, int nmb, int lane) {
     using F = Frag<DT>;
     const int lr = lane & 15;
     const int lg = lane >> 4;
     // 1. Q tile -> LDS;  2. B operands: column 16 nb + lr, window rows 8 lg .. 8 lg + 7.
     F qf[4];
+    F raw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (Q8)
+            raw[j] = W.q[j].template frag<DT>();
+        else
+            raw[j] = W.q[j];
+    }
     if constexpr (DT == LORA_BF16) {
         uint16_t* t = reinterpret_cast<uint16_t*>(tile);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(t + (lrow + j) * kQPitch + lcol) = W.q[j].q;
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(t + (lrow + j) * kQPitch + lcol) = raw[j].q;
         const int e = lr >> 2;
         const int c = lane & 3;
 #pragma unroll
@@ -192,7 +212,7 @@ __device__ __forceinline__ void contract_compute(const ContractWin<DT>& W, char*
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) t[(lcol + e) * kCtPitch + lrow + j] = W.q[j].get(e);
+            for (int e = 0; e < 8; ++e) t[(lcol + e) * kCtPitch + lrow + j] = raw[j].get(e);
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) qf[nb] = F::load_lds(t + (16 * nb + lr) * kCtPitch + 8 * lg);
     }
@@ -224,7 +244,8 @@ __device__ __forceinline__ void contract_compute(const ContractWin<DT>& W, char*
 // Body of workgroup blk of the G workgroups (NW waves each, G a multiple of
 // the 8 XCDs, workgroup blk placed at a launch index congruent to blk modulo
 // 8) that share the contraction; s_mem holds ContractLds<DT, NW>::kBytes.
-template <int DT, bool NT, int NW>
+// XQ: x is saved 8-bit rows.
+template <int DT, bool NT, int NW, bool XQ>
 __device__ __forceinline__ void contract_body(const ContractParams& p, int blk, int G, char* s_mem) {
     static_assert(NW >= 4, "waves 0..3 finish the four 16-column blocks of a tile");
     if (p.stop && *p.stop) return;
@@ -338,26 +359,33 @@ __device__ __forceinline__ void contract_body(const ContractParams& p, int blk, 
         if (nw > 0) {
             const int rot = cb_all % nw;
             auto win_at = [&](int i) { return wa + 32 * rotated(0, nw, rot, i < nw ? i : nw - 1); };
-            int32_t rowsA[4], rowsB[4];
-            ContractWin<DT> WA, WB;
-            contract_rows(rowsA, p.perm, win_at(0), lo, hi, lrow);
-            contract_rows(rowsB, p.perm, win_at(1), lo, hi, lrow);
-            contract_load<DT, NT>(WA, q, ldq, PT, p.ldT, rowsA, win_at(0), cq, lcol, rank0, r, lane);
-            contract_rows(rowsA, p.perm, win_at(2), lo, hi, lrow);
-            contract_load<DT, NT>(WB, q, ldq, PT, p.ldT, rowsB, win_at(1), cq, lcol, rank0, r, lane);
-            contract_rows(rowsB, p.perm, win_at(3), lo, hi, lrow);
-            // (B's multiply is unconditional inside the loop, so the compiler
-            // keeps B's loads where they are issued, a window ahead)
-            int i = 0;
-            for (; i + 1 < nw; i += 2) {
-                contract_compute<DT>(WA, tileA, acc, win_at(i), lo, hi, lcol, lrow, nmb, lane);
-                contract_load<DT, NT>(WA, q, ldq, PT, p.ldT, rowsA, win_at(i + 2), cq, lcol, rank0, r, lane);
-                contract_rows(rowsA, p.perm, win_at(i + 4), lo, hi, lrow);
-                contract_compute<DT>(WB, tileB, acc, win_at(i + 1), lo, hi, lcol, lrow, nmb, lane);
-                contract_load<DT, NT>(WB, q, ldq, PT, p.ldT, rowsB, win_at(i + 3), cq, lcol, rank0, r, lane);
-                contract_rows(rowsB, p.perm, win_at(i + 5), lo, hi, lrow);
-            }
-            if (i < nw) contract_compute<DT>(WA, tileA, acc, win_at(i), lo, hi, lcol, lrow, nmb, lane);
+            auto windows = [&](auto q8) {
+                constexpr bool Q8 = decltype(q8)::value;
+                int32_t rowsA[4], rowsB[4];
+                ContractWin<DT, Q8> WA, WB;
+                contract_rows(rowsA, p.perm, win_at(0), lo, hi, lrow);
+                contract_rows(rowsB, p.perm, win_at(1), lo, hi, lrow);
+                contract_load<DT, NT, Q8>(WA, q, ldq, p.xs, p.ldxs, PT, p.ldT, rowsA, win_at(0), cq, lcol, rank0, r, lane);
+                contract_rows(rowsA, p.perm, win_at(2), lo, hi, lrow);
+                contract_load<DT, NT, Q8>(WB, q, ldq, p.xs, p.ldxs, PT, p.ldT, rowsB, win_at(1), cq, lcol, rank0, r, lane);
+                contract_rows(rowsB, p.perm, win_at(3), lo, hi, lrow);
+                // (B's multiply is unconditional inside the loop, so the compiler
+                // keeps B's loads where they are issued, a window ahead)
+                int i = 0;
+                for (; i + 1 < nw; i += 2) {
+                    contract_compute<DT, Q8>(WA, tileA, acc, win_at(i), lo, hi, lcol, lrow, nmb, lane);
+                    contract_load<DT, NT, Q8>(WA, q, ldq, p.xs, p.ldxs, PT, p.ldT, rowsA, win_at(i + 2), cq, lcol, rank0, r, lane);
+                    contract_rows(rowsA, p.perm, win_at(i + 4), lo, hi, lrow);
+                    contract_compute<DT, Q8>(WB, tileB, acc, win_at(i + 1), lo, hi, lcol, lrow, nmb, lane);
+                    contract_load<DT, NT, Q8>(WB, q, ldq, p.xs, p.ldxs, PT, p.ldT, rowsB, win_at(i + 3), cq, lcol, rank0, r, lane);
+                    contract_rows(rowsB, p.perm, win_at(i + 5), lo, hi, lrow);
+                }
+                if (i < nw) contract_compute<DT, Q8>(WA, tileA, acc, win_at(i), lo, hi, lcol, lrow, nmb, lane);
+            };
+            if (XQ && is_dA)
+                windows(std::bool_constant<XQ>{});
+            else
+                windows(std::false_type{});
         }
 
         // Fixed-order sum of the waves' tiles; wave nb (< 4) finishes column block nb.

@@ -21,6 +21,7 @@ namespace lora {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // Pointers into device memory that the compiler cannot prove global (e.g.
 // the adapter weights, read from the device-resident table) would otherwise
@@ -370,6 +371,25 @@ __device__ __forceinline__ u32x4_t buf_load16(buf_rsrc_t r, uint32_t voff, uint3
 // should not push out of L2 the lines other workgroups still re-read).
 __device__ __forceinline__ u32x4_t buf_load16_nt(buf_rsrc_t r, uint32_t voff, uint32_t soff) {
     return __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 2);
+}
+
+// A buffer load of `bytes` (4 or 16) per lane straight into LDS: lane L's
+// bytes land at lds + bytes * L (lds wave-uniform); bytes past the buffer
+// (voff) are not fetched.  soff (wave-uniform) adds to the memory address
+// only.  Issued from assembly: the compiler does not track it, so the caller
+// waits (vmcnt) before any read of those LDS bytes and before reusing them.
+__device__ __forceinline__ void dma_lds(buf_rsrc_t r, uint32_t voff, uint32_t soff, void* lds, int bytes) {
+    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    if (bytes == 16)
+        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :
+                     : "s"(m0), "v"(voff), "s"(r), "s"(soff)
+                     : "memory", "m0");
+    else
+        asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+                     :
+                     : "s"(m0), "v"(voff), "s"(r), "s"(soff)
+                     : "memory", "m0");
 }
 
 // s_waitcnt vmcnt(N) with the other counters left alone (gfx9 encoding:

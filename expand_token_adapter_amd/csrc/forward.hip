@@ -26,9 +26,11 @@ constexpr int64_t kShrinkMaxGrid = 512;
 template <int DT, int RB>
 void launch_shrink_rb(bool trans_w, const ShrinkParams& p, unsigned grid, hipStream_t st) {
     if (trans_w)
-        hipLaunchKernelGGL((shrink_kernel<DT, true, RB>), dim3(grid), dim3(kShrinkThreads), 0, st, p);
+        hipLaunchKernelGGL((shrink_kernel<DT, true, RB, false>), dim3(grid), dim3(kShrinkThreads), 0, st, p);
+    else if (p.xs)
+        hipLaunchKernelGGL((shrink_kernel<DT, false, RB, true>), dim3(grid), dim3(kShrinkThreads), 0, st, p);
     else
-        hipLaunchKernelGGL((shrink_kernel<DT, false, RB>), dim3(grid), dim3(kShrinkThreads), 0, st, p);
+        hipLaunchKernelGGL((shrink_kernel<DT, false, RB, false>), dim3(grid), dim3(kShrinkThreads), 0, st, p);
 }
 
 // 16-rank blocks per task: 1 (r_max <= 16), 2 (<= 32), else 4 (64-rank groups)

@@ -7,7 +7,10 @@
 // order, so results are bit-reproducible.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
+#include "quant.h"
 
 namespace lora {
 
@@ -44,8 +47,10 @@ __host__ __device__ constexpr int shrink_slices(int dtype, int K) {
 }
 
 struct ShrinkParams {
-    const void* x;   // rows gathered through perm
+    const void* x;   // rows gathered through perm (saved 8-bit rows: their codes)
     int64_t ldx;
+    const uint8_t* xs;  // scales of saved 8-bit rows
+    int64_t ldxs;
     int32_t K;       // reduction length (d_in, or d_out for g)
     const lora_adapter* adapters;
     int32_t r_max;
@@ -65,8 +70,8 @@ struct ShrinkParams {
 
 // acc[mb] += W(rank block mb) x X over chunks cc0 .. cc0 + SCH - 1 of the slice
 // (chunks >= nch and K offsets >= klen contribute nothing).
-template <int DT, int SCH, int NMB>
-__device__ __forceinline__ void shrink_slice_mma(f32x4_t* acc, const Frag<DT> (*xr)[2], const u32x4_t* s_w, int cc0,
+template <int DT, int SCH, int NMB, class X>
+__device__ __forceinline__ void shrink_slice_mma(f32x4_t* acc, const X (*xr)[2], const u32x4_t* s_w, int cc0,
                                                  int nch, int klen, int lr, int lg) {
     using F = Frag<DT>;
 #pragma unroll
@@ -76,7 +81,12 @@ __device__ __forceinline__ void shrink_slice_mma(f32x4_t* acc, const Frag<DT> (*
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int kk = cc * 64 + 8 * lg + 32 * h;
-                const F xf = kk < klen ? xr[c][h] : F::zero();
+                F xf = F::zero();
+                if constexpr (std::is_same_v<X, QuantRaw>) {
+                    if (kk < klen) xf = xr[c][h].template frag<DT>();
+                } else {
+                    if (kk < klen) xf = xr[c][h];
+                }
 #pragma unroll
                 for (int mb = 0; mb < NMB; ++mb) {
                     const u32x4_t* wrow = s_w + (16 * mb + lr) * 64;
@@ -97,8 +107,8 @@ __device__ __forceinline__ void shrink_slice_mma(f32x4_t* acc, const Frag<DT> (*
 
 // RB: 16-rank blocks a task covers (1, 2 or 4, from r_max): the weight slice
 // in LDS (16 RB rank rows of 1 KB) and the accumulators are sized for it, so
-// small ranks leave room for more workgroups per CU.
-template <int DT, bool TRANS_W, int RB>
+// small ranks leave room for more workgroups per CU.  XQ: x is saved 8-bit rows.
+template <int DT, bool TRANS_W, int RB, bool XQ>
 __global__ __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4)))
 void shrink_kernel(ShrinkParams p) {
     using F = Frag<DT>;
@@ -199,16 +209,21 @@ void shrink_kernel(ShrinkParams p) {
 
         // 1. This wave's x half-slice (chunk c, half h; chunks past the slice
         //    re-read its start), then the weight slice loads (16-byte units).
-        F xr[SCH][2];
+        std::conditional_t<XQ, QuantRaw, F> xr[SCH][2];
         if (work) {
-            const char* xp = static_cast<const char*>(p.x) + xrow * p.ldx * EB;
+            const char* xp = static_cast<const char*>(p.x) + xrow * p.ldx * (XQ ? 1 : EB);
+            const uint8_t* xsp = XQ ? p.xs + xrow * p.ldxs : nullptr;
 #pragma unroll
             for (int c = 0; c < SCH; ++c)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int cc = kh * SCH + c;
                     const int kk = (cc < nch ? cc * 64 : 0) + 8 * lg + 32 * h;
-                    xr[c][h] = F::load(xp + (int64_t)(k0 + (kk < klen ? kk : 0)) * EB);
+                    const int k = k0 + (kk < klen ? kk : 0);
+                    if constexpr (XQ)
+                        xr[c][h] = QuantRaw::load(reinterpret_cast<const uint8_t*>(xp), xsp, k);
+                    else
+                        xr[c][h] = F::load(xp + (int64_t)k * EB);
                 }
             if constexpr (!TRANS_W) {
                 // Straight into LDS, issued last (the compiler does not track

@@ -423,6 +423,101 @@ typedef struct {
 int lora_adamw_step(int dtype, const lora_adamw_tensor* tensors, int32_t n_tensors, lora_adamw_params hp,
                     void* stream);
 
+/* ------------------------------------------------------------------ 8-bit rows and weights
+ *
+ * Fine-tuning keeps the layer input x of every fine-tuning row until its
+ * backward, and saved activations dominate the memory of a fine-tuning step
+ * (DeltaServe, section 3.2, "Mixed forward batch"; MOLT, section 1).  The
+ * calls below hold such rows, and the frozen weight W of h(x) = W x + B A x,
+ * in 8-bit floating point, compute the base product from them and run the LoRA
+ * backward on the saved rows directly.
+ *
+ * lora_quant: a matrix of rows x cols values,
+ *     value[i][j] = code[i][j] * 2^(scale - 127)
+ *   codes  [rows, ld]  e4m3 (1 sign, 4 exponent, 3 fraction bits, bias 7;
+ *          largest 448, no infinities, 0x7f and 0xff are NaN), 16-byte
+ *          aligned, ld >= round_up(cols, 128) and a multiple of 128.  The codes
+ *          of columns cols .. round_up(cols, 128) - 1 are zeros: the calls that
+ *          write codes write them, and the calls that read codes rely on it.
+ *   scales [.., lds]   one exponent byte per block of 128 (255 is NaN), 4-byte
+ *          aligned, lds >= ceil(cols / 128) and a multiple of 4.
+ *          Rows (activations): one row of scales per row, block j = columns
+ *          128 j .. 128 j + 127.  Weights: one row of scales per 128 rows, so a
+ *          scale covers 128 x 128 values and the transposed weight has the
+ *          transposed codes and scales.
+ *   cols a multiple of 8.  Bytes of scales past ceil(cols / 128) are not used.
+ * A block's scale is the smallest power of two, 2^-127 at the least, that
+ * brings its largest finite magnitude to 448 or less (1 for a block without
+ * one); codes are rounded to nearest, ties to even; what is not finite becomes
+ * NaN and does not enter the scale.
+ */
+#define LORA_QUANT_BLOCK 128
+#define LORA_QUANT_MAX_LD (1 << 22) /* largest ld of lora_base_product's operands */
+
+typedef struct lora_quant {
+    uint8_t* codes;
+    int64_t ld;
+    uint8_t* scales;
+    int64_t lds;
+} lora_quant;
+
+/*
+ * Save rows: q = the 8-bit form of x [T, ldx] (dtype), d columns.  One kernel.
+ * A range of a longer matrix is saved by pointer offsets of x and q (a row of
+ * q is a row of codes and a row of scales).
+ */
+int lora_quant_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, lora_quant q, void* stream);
+
+/*
+ * Restore rows: x [T, ldx] (dtype) = the values of q, d columns (bf16: exact
+ * for scale bytes from 3 to 246, else rounded to nearest even).  One kernel.
+ */
+int lora_dequant_rows(int dtype, lora_quant q, int32_t T, int32_t d, void* x, int64_t ldx, void* stream);
+
+/*
+ * 8-bit form of a weight w [d_out, ldw] (dtype, d_in columns), in blocks of
+ * 128 x 128.  transpose = 0: q is [d_out, d_in].  transpose = 1: q is the
+ * transposed weight [d_in, d_out], with the transposed codes and scales of
+ * the other form, for products with W^T (dX = W^T dY).  d_out and d_in
+ * multiples of 8.  One kernel, once per weight.
+ */
+int lora_quant_weight(int dtype, const void* w, int64_t ldw, int32_t d_out, int32_t d_in, int32_t transpose,
+                      lora_quant q, void* stream);
+
+/* Workspace bytes of lora_base_product (host, pure). */
+size_t lora_base_product_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out);
+
+/*
+ * Base product: y_t = W x_t (accumulate = 0) or y_t += W x_t (accumulate = 1),
+ * the frozen part of h(x) = W x + B A x (MOLT, section 2.1), for every row of
+ * x, with fp32 sums rounded once to y's type.
+ *   x: 8-bit rows [T, d_in]; w: 8-bit weight [d_out, d_in]; y [T, ldy] (dtype).
+ *   With x = the 8-bit rows of dY and w = the transposed weight it is the base
+ *   part of the backward, dX (+)= W^T dY.
+ *   ws: lora_base_product_workspace_bytes(T, d_in, d_out) bytes.
+ * Rows are independent: a NaN in one does not reach another.  The order of
+ * every sum is fixed by the shapes: results are bit-reproducible.
+ */
+int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
+                      int64_t ldy, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of lora_backward_quant (host, pure). */
+size_t lora_backward_quant_workspace_bytes(int dtype, int32_t T_ft, int32_t d_in, int32_t d_out, int32_t r_max);
+
+/*
+ * lora_backward from saved 8-bit rows: x holds the layer input of the
+ * fine-tuning rows as lora_quant_rows saved it and is read as it is; nothing
+ * is restored to memory.  dtype is the type of dy, dx, A and B.  Every other
+ * argument, result and error as for lora_backward; the results equal those of
+ * lora_backward on the restored rows (lora_dequant_rows) bit for bit.  v_saved
+ * is best v = A x as the forward computed it; NULL recomputes it from the
+ * saved rows.
+ */
+int lora_backward_quant(int dtype, lora_quant x, const void* dy, int64_t lddy, void* dx, int64_t lddx, int32_t T_ft,
+                        int32_t d_in, int32_t d_out, const lora_adapter* adapters, const lora_adapter_grad* grads,
+                        int32_t num_adapters, int32_t r_max, lora_segments seg_ft, const float* v_saved, int64_t ldv,
+                        void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
