@@ -20,10 +20,15 @@
 // v_mfma_f32_16x16x32_bf16 sums their exact products in fp32.
 //
 // A operand = weight rows (n), B operand = activation rows (t), so a lane ends
-// with four consecutive n of one row t.  The order of the 128 products inside
+// with four operand rows of one t.  Which weight row is which operand row is
+// free as well: blocks are taken in pairs of 32 rows, operand row 4 g + i of
+// block b of the pair is row 8 g + 4 b + i, so a lane's two times four outputs
+// are eight consecutive n (one 16-byte store of bf16).  The order of the 128 products inside
 // a block is free (both operands take the same one): lane group g = lane / 16
 // takes the 16-byte units g and g + 4 of each 128-byte block row.
 #pragma once
+
+#include <type_traits>
 
 #include "quant.h"
 
@@ -45,33 +50,42 @@ struct BaseParams {
     int32_t T, N, nkb;  // rows, outputs, blocks of 128 along k
     int32_t accumulate;
     int32_t tiles_n, tiles_t;
+    int32_t splits;  // parts of k, each a workgroup's; more than one: fp32 sums to part
+    float* part;     // [splits][T][N]
 };
 
-// One operand row's block of 128: this lane's 32 codes and the row's scale
-// byte (bits 7:0 of scale; the others do not count).
+// One operand row's block of 128: this lane's 32 codes.
+struct QuantOperand {
+    u32x4_t u[2];
+};
+// The same as an operand of the matrix instruction.  The scale comes as a word
+// of four blocks' bytes and the place Q of this block's byte in it.
 template <int DT>
 struct QuantFrag;
 template <>
 struct QuantFrag<LORA_BF16> {
     i32x8_t codes;
     int scale;
-    __device__ __forceinline__ static QuantFrag make(u32x4_t u0, u32x4_t u1, uint32_t scale) {
-        return QuantFrag{i32x8_t{(int)u0[0], (int)u0[1], (int)u0[2], (int)u0[3], (int)u1[0], (int)u1[1], (int)u1[2],
-                                 (int)u1[3]},
+    template <int Q>
+    __device__ __forceinline__ static QuantFrag make(const QuantOperand& o, uint32_t scale) {
+        return QuantFrag{__builtin_bit_cast(i32x8_t, __builtin_shufflevector(o.u[0], o.u[1], 0, 1, 2, 3, 4, 5, 6, 7)),
                          (int)scale};
     }
+    template <int Q>
     __device__ __forceinline__ f32x4_t mma(const QuantFrag& b, f32x4_t c) const {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes, b.codes, c, 0, 0, 0, scale, 0, b.scale);
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes, b.codes, c, 0, 0, Q, scale, Q, b.scale);
     }
 };
 template <>
 struct QuantFrag<LORA_F32> {
     Frag<LORA_BF16> q[4];
-    __device__ __forceinline__ static QuantFrag make(u32x4_t u0, u32x4_t u1, uint32_t scale) {
-        const float s = quant_scale(scale & 255u);
-        return QuantFrag{{dequant8<LORA_BF16>(u0[0], u0[1], s), dequant8<LORA_BF16>(u0[2], u0[3], s),
-                          dequant8<LORA_BF16>(u1[0], u1[1], s), dequant8<LORA_BF16>(u1[2], u1[3], s)}};
+    template <int Q>
+    __device__ __forceinline__ static QuantFrag make(const QuantOperand& o, uint32_t scale) {
+        const float s = quant_scale((scale >> (8 * Q)) & 255u);
+        return QuantFrag{{dequant8<LORA_BF16>(o.u[0][0], o.u[0][1], s), dequant8<LORA_BF16>(o.u[0][2], o.u[0][3], s),
+                          dequant8<LORA_BF16>(o.u[1][0], o.u[1][1], s), dequant8<LORA_BF16>(o.u[1][2], o.u[1][3], s)}};
     }
+    template <int Q>
     __device__ __forceinline__ f32x4_t mma(const QuantFrag& b, f32x4_t c) const {
 #pragma unroll
         for (int i = 0; i < 4; ++i) c = lora::mma(q[i], b.q[i], c);
@@ -79,13 +93,29 @@ struct QuantFrag<LORA_F32> {
     }
 };
 
-// Four consecutive outputs of one row: added to what is there (accumulate) in
+// Eight consecutive outputs of one row: added to what is there (accumulate) in
 // fp32, rounded once.
 template <int DT>
+__device__ __forceinline__ void base_store8(const BaseParams& p, int t, int n, f32x4_t v0, f32x4_t v1) {
+    if (t >= p.T || n >= p.N) return;  // (N is a multiple of 8: the eight are in or out together)
+    char* at = p.y + ((int64_t)t * p.ldy + n) * Frag<DT>::kBytes;
+    float f[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
+    if (p.accumulate) {
+        float o[8];
+        Elem<DT>::load8(at, o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += o[e];
+    }
+    Elem<DT>::store8(at, f);
+}
+
+// Four of them.
+template <int DT>
 __device__ __forceinline__ void base_store4(const BaseParams& p, int t, int n, f32x4_t v) {
-    if (t >= p.T || n >= p.N) return;  // (N is a multiple of 8: the four are in or out together)
+    if (t >= p.T || n >= p.N) return;
+    char* at = p.y + ((int64_t)t * p.ldy + n) * Frag<DT>::kBytes;
     if constexpr (DT == LORA_BF16) {
-        LORA_GLOBAL u32x2_t* d = gptr(reinterpret_cast<u32x2_t*>(p.y + ((int64_t)t * p.ldy + n) * 2));
+        LORA_GLOBAL u32x2_t* d = gptr(reinterpret_cast<u32x2_t*>(at));
         if (p.accumulate) {
             const u32x2_t o = *d;
             v += f32x4_t{__uint_as_float(o[0] << 16), __uint_as_float(o[0] & 0xffff0000u), __uint_as_float(o[1] << 16),
@@ -93,7 +123,7 @@ __device__ __forceinline__ void base_store4(const BaseParams& p, int t, int n, f
         }
         *d = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     } else {
-        LORA_GLOBAL f32x4_t* d = gptr(reinterpret_cast<f32x4_t*>(p.y + ((int64_t)t * p.ldy + n) * 4));
+        LORA_GLOBAL f32x4_t* d = gptr(reinterpret_cast<f32x4_t*>(at));
         if (p.accumulate) v += *d;
         *d = v;
     }
@@ -104,63 +134,81 @@ __device__ __forceinline__ void base_store4(const BaseParams& p, int t, int n, f
 // A workgroup of WN x WT waves computes BN outputs x BT rows.  A step is one
 // block of 128 along k: BN + BT block rows of 128 bytes go from memory straight
 // into LDS, ST stages in a ring, the loads of step i + ST - 1 issued while step
-// i is multiplied.  Unit c (16 bytes) of row r lies at position c ^ (r % 8) of
-// the row, so that the 16 rows of an operand read fall on different banks.
-// The scales of up to kBaseGroups * 4 blocks lie in LDS too, four blocks' bytes
-// of one row in a word; a longer k is taken in pieces.
+// i is multiplied.  Unit c (16 bytes) of a row lies at position c ^ s of the
+// row, s the operand row modulo 8 that the row becomes, so that the rows that a
+// read takes together fall on different banks.
+// The scales of up to BaseLds::kGroups * 4 blocks lie in LDS too, four blocks'
+// bytes of one row in a word; a longer k is taken in pieces.
 
-constexpr int kBaseGroups = 30;
+constexpr int kLdsBytes = 160 * 1024;  // of a CU
+constexpr int kBand = 4;
 
 template <int BN, int BT, int ST>
 struct BaseLds {
     static constexpr int kStage = (BN + BT) * kQBlock;
-    static constexpr int kScales = kBaseGroups * (BT + BN / 16) * 4;
-    static constexpr int kBytes = ST * kStage + kScales;
+    static constexpr int kNB = BN > kQBlock ? BN / kQBlock : 1;  // 128-row blocks of the weight tile
+    static constexpr int kWeight = kNB * kWave * 4;              // bytes of the weight's scale words
+    static constexpr int kFit = (kLdsBytes - ST * kStage - kWeight) / (BT * 4);
+    static constexpr int kGroups = kFit < 32 ? kFit : 32;
+    static constexpr int kBytes = ST * kStage + kWeight + kGroups * BT * 4;
+    static_assert(kGroups >= 8, "room for the scales of 4096 columns");
 };
 
 template <int BN, int BT, int WN, int WT, int ST, int DT>
 __global__ __launch_bounds__(WN* WT* kWave) void base_kernel(BaseParams p) {
+    using L = BaseLds<BN, BT, ST>;
     constexpr int NW = WN * WT;
     constexpr int FN = BN / WN / 16, FT = BT / WT / 16;  // 16 x 16 blocks of a wave
-    constexpr int UN = BN / 8, UT = BT / 8;              // 1 KB loads of a stage
-    constexpr int PW = (UN + UT) / NW;                   // loads of a wave and stage
-    constexpr int NB = BN / 16;                          // weight scale words per group, one for each 16 outputs
-    static_assert(UN % NW == 0 && UT % NW == 0, "every wave loads the same number of rows");
-    using L = BaseLds<BN, BT, ST>;
+    constexpr int GA = 2, NG = FN / GA;         // weight blocks of a group, groups
+    constexpr int WU = 4 / WT, XU = BT / 8 / NW;  // loads of a wave per weight group, for the activations
+    constexpr int PW = NG * WU + XU;            // of a step
+    constexpr int NB = L::kNB;                  // 128-row blocks of the weight tile
+    static_assert(FN % 2 == 0 && NW % 4 == 0 && 4 % WT == 0 && BT % (8 * NW) == 0, "the loads divide evenly");
+    static_assert(BN / WN <= kQBlock, "a wave's outputs lie in one block of 128 weight rows");
     __shared__ __attribute__((aligned(16))) char s_lds[L::kBytes];
     uint32_t* s_xs = reinterpret_cast<uint32_t*>(s_lds + ST * L::kStage);  // [group][BT]
-    uint32_t* s_ws = s_xs + kBaseGroups * BT;                              // [group][NB]
+    uint32_t* s_ws = s_xs + L::kGroups * BT;                              // [128-row block][64 groups]
 
     const int wave = wave_id();
     const int lane = threadIdx.x & (kWave - 1);
     const int lr = lane & 15, lg = lane >> 4;
     // Workgroups of one XCD take neighbouring tiles.
-    const int ntile = p.tiles_n * p.tiles_t;
+    const int ntile = p.tiles_n * p.tiles_t * p.splits;
     const int per = (ntile + kNumXcd - 1) / kNumXcd;
-    const int tile = (int)(blockIdx.x % kNumXcd) * per + (int)(blockIdx.x / kNumXcd);
-    if ((int)(blockIdx.x / kNumXcd) >= per || tile >= ntile) return;
-    const int n0 = (tile % p.tiles_n) * BN, t0 = (tile / p.tiles_n) * BT;
+    const int task = (int)(blockIdx.x % kNumXcd) * per + (int)(blockIdx.x / kNumXcd);
+    if ((int)(blockIdx.x / kNumXcd) >= per || task >= ntile) return;
+    const int tile = task / p.splits, part = task - tile * p.splits;
+    // this workgroup's blocks along k: whole words of scales
+    const int ngr = (p.nkb + 3) / 4;
+    const int kb0 = 4 * (int)((int64_t)ngr * part / p.splits);
+    const int kb1 = min(p.nkb, 4 * (int)((int64_t)ngr * (part + 1) / p.splits));
+    // Order of the tiles: bands of up to kBand tiles along t, walked along n, so
+    // that the 32 tiles in flight on an XCD share few weight and activation rows.
+    const int band = tile / (kBand * p.tiles_n), in = tile - band * kBand * p.tiles_n;
+    const int bt = min(kBand, p.tiles_t - band * kBand);
+    const int n0 = in / bt * BN, t0 = (band * kBand + in % bt) * BT;
     const int wn = (wave % WN) * (BN / WN), wt = (wave / WN) * (BT / WT);
 
-    // Loads: wave w takes the 8-row units w, w + NW, ...; rows past the matrix
-    // repeat its last row (their outputs are not stored).
+    // The loads of a stage, 8 rows each: WU a wave for the weight rows that the
+    // waves read as group g (rows 32 g .. + 31 of every wave column), XU for the
+    // activation rows.  Rows past the matrix lie past their buffer: nothing is
+    // fetched for them, and their outputs are not stored.
     const int nrows = min(BN, p.N - n0), trows = min(BT, p.T - t0);
     const buf_rsrc_t rw = make_rsrc(p.w + (int64_t)n0 * p.ldw, (uint32_t)((nrows - 1) * p.ldw + (int64_t)p.nkb * kQBlock));
     const buf_rsrc_t rx = make_rsrc(p.x + (int64_t)t0 * p.ldx, (uint32_t)((trows - 1) * p.ldx + (int64_t)p.nkb * kQBlock));
-    uint32_t voff[PW];
-#pragma unroll
-    for (int j = 0; j < PW; ++j) {
-        const int r8 = lane >> 3;
-        const int row = 8 * (wave + NW * j) + r8;  // of the stage: BN weight rows, then BT activation rows
-        const uint32_t unit = (uint32_t)((lane & 7) ^ r8) * 16u;
-        voff[j] = NW * j < UN ? (uint32_t)(min(row, nrows - 1) * p.ldw) + unit
-                              : (uint32_t)(min(row - BN, trows - 1) * p.ldx) + unit;
-    }
-    auto issue = [&](int slot, int kb) {
-        char* at = s_lds + slot * L::kStage + wave * 1024;
-#pragma unroll
-        for (int j = 0; j < PW; ++j)
-            dma_lds(NW * j < UN ? rw : rx, voff[j], (uint32_t)kb * kQBlock, at + NW * j * 1024, 16);
+    const int w_row = wave / 4 * (BN / WN) + 8 * (wave & 3), x_row = 8 * wave, r8 = lane >> 3;
+    const uint32_t vw = (uint32_t)((w_row + r8) * p.ldw) + (uint32_t)((lane & 7) ^ (r8 & 3) ^ (wave & 1) * 4) * 16u;
+    const uint32_t vx = (uint32_t)((x_row + r8) * p.ldx) + (uint32_t)((lane & 7) ^ r8) * 16u;
+    // Load o of a stage: those of weight group 0, of the activations, of weight groups 1, 2, ...
+    auto issue = [&](int o, int slot, int kb) {
+        const bool w = o < WU || o >= WU + XU;
+        const int ow = o < WU ? o : o - XU;
+        const int row = w ? 32 * (ow / WU) + NW / 4 * (ow % WU) * (BN / WN) : 8 * NW * (o - WU);
+        char* at = s_lds + slot * L::kStage + (w ? w_row + row : BN + x_row + row) * kQBlock;
+        if (w)
+            dma_lds(rw, vw + (uint32_t)(row * p.ldw), (uint32_t)kb * kQBlock, at, 16);
+        else
+            dma_lds(rx, vx + (uint32_t)(row * p.ldx), (uint32_t)kb * kQBlock, at, 16);
     };
 
     f32x4_t acc[FN][FT];
@@ -170,57 +218,222 @@ __global__ __launch_bounds__(WN* WT* kWave) void base_kernel(BaseParams p) {
         for (int b = 0; b < FT; ++b) acc[a][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     // This lane's operand bytes of a block row: units lg and lg + 4.
     const int lrow = lr * kQBlock + ((lg ^ (lr & 7)) * 16);
+    const int lrow_w = (8 * (lr >> 2) + (lr & 3)) * kQBlock + ((lg ^ (lr & 7)) * 16);
+    QuantOperand b[FT], a[2][GA];
+    uint32_t xs[FT], ws;  // scale words
+    // half u of a block row: unit lg (u = 0) or lg + 4 (u = 1)
+    auto read_b = [&](int f, int u, int slot) {
+        b[f].u[u] = *reinterpret_cast<const u32x4_t*>(s_lds + slot * L::kStage + (BN + wt + 16 * f) * kQBlock +
+                                                      (u ? lrow ^ 64 : lrow));
+    };
+    auto read_a = [&](QuantOperand* q, int f, int u, int slot, int grp) {
+        const int blk = GA * grp + f;
+        q[f].u[u] = *reinterpret_cast<const u32x4_t*>(s_lds + slot * L::kStage + (wn + 32 * (blk / 2) + 4 * (blk & 1)) * kQBlock +
+                                                      (u ? lrow_w ^ 64 : lrow_w));
+    };
+    auto read_xs = [&](int f, int grp) { xs[f] = s_xs[grp * BT + wt + 16 * f + lr]; };
+    auto read_ws = [&](uint32_t& to, int grp) { to = s_ws[wn / kQBlock * kWave + grp]; };
 
-    for (int k0 = 0; k0 < p.nkb; k0 += 4 * kBaseGroups) {
-        const int k1 = min(p.nkb, k0 + 4 * kBaseGroups);
-        const int ng = (k1 - k0 + 3) / 4;
-        if (k0 > 0) {
+    for (int k0 = kb0; k0 < kb1; k0 += 4 * L::kGroups) {
+        const int nk = min(kb1 - k0, 4 * L::kGroups);  // steps of this piece
+        const int ng = (nk + 3) / 4;
+        if (k0 > kb0) {
             wait_vmcnt_le<0>();
             lds_barrier();  // the last piece's stages and scales are no longer read
         }
-        for (int i = threadIdx.x; i < ng * BT; i += NW * kWave) {
-            const int g = i % ng, t = min(i / ng, trows - 1);
-            s_xs[g * BT + i / ng] = *gptr(reinterpret_cast<const uint32_t*>(p.xs + (int64_t)(t0 + t) * p.ldxs + k0 + 4 * g));
+        // scale words, a load for 64 rows of one group (activations) or for the
+        // groups of one 128-row block (weight); past the matrix: the last row's
+        for (int c = wave; c < ng * (BT / kWave); c += NW) {
+            const int g = c / (BT / kWave), t = c % (BT / kWave) * kWave;
+            lds_dma4_async(p.xs + (int64_t)(t0 + min(t + lane, trows - 1)) * p.ldxs + k0 + 4 * g, s_xs + g * BT + t);
         }
-        for (int i = threadIdx.x; i < ng * NB; i += NW * kWave) {
-            const int g = i / NB, b = i % NB;
-            const int nblk = min(n0 + 16 * b, p.N - 1) / kQBlock;
-            s_ws[i] = *gptr(reinterpret_cast<const uint32_t*>(p.ws + (int64_t)nblk * p.ldws + k0 + 4 * g));
+        if (wave < NB) {
+            const int nblk = min(n0 + kQBlock * wave, p.N - 1) / kQBlock;
+            lds_dma4_async(p.ws + (int64_t)nblk * p.ldws + k0 + 4 * min(lane, ng - 1), s_ws + wave * kWave);
         }
         // (loads past the piece repeat its last block: every step waits for the same number)
 #pragma unroll
-        for (int s = 0; s < ST - 1; ++s) issue(s, min(k0 + s, k1 - 1));
+        for (int s = 0; s < ST; ++s)
+#pragma unroll
+            for (int o = 0; o < PW; ++o) issue(o, s, k0 + min(s, nk - 1));
+        wait_vmcnt_le<PW*(ST - 1)>();
+        lds_barrier();
+#pragma unroll
+        for (int f = 0; f < GA; ++f)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) read_a(a[0], f, u, 0, 0);
+#pragma unroll
+        for (int f = 0; f < FT; ++f) {
+            read_b(f, 0, 0);
+            read_b(f, 1, 0);
+            read_xs(f, 0);
+        }
+        read_ws(ws, 0);
         int slot = 0;
-        for (int kb = k0; kb < k1; ++kb) {
-            wait_vmcnt_le<PW*(ST - 2)>();
-            lds_barrier();
-            issue(slot == 0 ? ST - 1 : slot - 1, min(kb + ST - 1, k1 - 1));
-            const char* sw = s_lds + slot * L::kStage + wn * kQBlock;
-            const char* sx = s_lds + slot * L::kStage + (BN + wt) * kQBlock;
-            const int g = (kb - k0) >> 2, sh = 8 * ((kb - k0) & 3);
-            QuantFrag<DT> b[FT];
+        // One step (Q: its number modulo 4).  The weight blocks are taken GA at a
+        // time; while a group is multiplied the next one is read, and with the
+        // last group the next step's first group and activations.  After the
+        // barrier at the start of group g every wave has that group in registers,
+        // so its place in the stage is free (with group 0 the activations' too) and
+        // the loads of step i + ST can go there, spread over the groups: they have
+        // nearly ST steps to land, not ST - 1 as with one barrier and all loads at
+        // the step's end (4096 rows, 14336 -> 4096: 166 against 188 us).
+        // Reads and loads go between products, a few at a time: a burst after the
+        // barrier would leave the matrix cores without work meanwhile.
+        // the loads of a step that go out before its group g
+        constexpr auto before = [](int g) { return PW * g / NG; };
+        auto step = [&](auto quarter, int i) {
+            constexpr int Q = decltype(quarter)::value;
+            const int next = slot + 1 == ST ? 0 : slot + 1;
+            const int kn = k0 + min(i + ST, nk - 1);
+            uint32_t ws_next = ws;
+            auto group = [&](auto gc) {
+                constexpr int g = decltype(gc)::value;
+                constexpr bool last = g + 1 == NG;
+                QuantOperand* cur = a[(Q * NG + g) & 1];
+                QuantOperand* nxt = a[(Q * NG + g + 1) & 1];
+                // What is read now has to be there: the loads issued after it may be
+                // outstanding.
+                wait_vmcnt_le<last ? (NG - 1) * WU + (ST - 2) * PW + before(NG - 1)
+                                   : (NG - 2 - g) * WU + (ST - 1) * PW + before(g)>();
+                lds_barrier();
+                QuantFrag<DT> af[GA];
 #pragma unroll
-            for (int f = 0; f < FT; ++f)
-                b[f] = QuantFrag<DT>::make(*reinterpret_cast<const u32x4_t*>(sx + f * 16 * kQBlock + lrow),
-                                           *reinterpret_cast<const u32x4_t*>(sx + f * 16 * kQBlock + (lrow ^ 64)),
-                                           s_xs[g * BT + wt + 16 * f + lr] >> sh);
+                for (int f = 0; f < GA; ++f) af[f] = QuantFrag<DT>::template make<Q>(cur[f], ws);
 #pragma unroll
-            for (int f = 0; f < FN; ++f) {
-                const QuantFrag<DT> a =
-                    QuantFrag<DT>::make(*reinterpret_cast<const u32x4_t*>(sw + f * 16 * kQBlock + lrow),
-                                        *reinterpret_cast<const u32x4_t*>(sw + f * 16 * kQBlock + (lrow ^ 64)),
-                                        s_ws[g * NB + wn / 16 + f] >> sh);
+                for (int h = 0; h < FT; ++h) {
+                    const QuantFrag<DT> bf = QuantFrag<DT>::template make<Q>(b[h], xs[h]);
 #pragma unroll
-                for (int h = 0; h < FT; ++h) acc[f][h] = a.mma(b[h], acc[f][h]);
-            }
-            slot = slot + 1 == ST ? 0 : slot + 1;
+                    for (int f = 0; f < GA; ++f)
+                        acc[GA * g + f][h] = af[f].template mma<Q>(bf, acc[GA * g + f][h]);
+#pragma unroll
+                    for (int r = h * 2 * GA / FT; r < (h + 1) * 2 * GA / FT; ++r)
+                        read_a(nxt, r >> 1, r & 1, last ? next : slot, last ? 0 : g + 1);
+                    if (last) {
+                        read_b(h, 0, next);
+                        read_b(h, 1, next);
+                        if (Q == 3) read_xs(h, min(i + 1, nk - 1) >> 2);
+                        if (Q == 3 && h == 0) read_ws(ws_next, min(i + 1, nk - 1) >> 2);
+                    }
+                    constexpr int o0 = before(g), n = before(g + 1) - o0;
+#pragma unroll
+                    for (int o = o0 + h * n / FT; o < o0 + (h + 1) * n / FT; ++o) issue(o, slot, kn);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            group(std::integral_constant<int, 0>{});
+            if constexpr (NG > 1) group(std::integral_constant<int, 1 % NG>{});
+            if constexpr (NG > 2) group(std::integral_constant<int, 2 % NG>{});
+            if constexpr (NG > 3) group(std::integral_constant<int, 3 % NG>{});
+            static_assert(NG <= 4, "groups");
+            ws = ws_next;
+            slot = next;
+        };
+        for (int i = 0; i < nk; i += 4) {
+            step(std::integral_constant<int, 0>{}, i);
+            if (i + 1 < nk) step(std::integral_constant<int, 1>{}, i + 1);
+            if (i + 2 < nk) step(std::integral_constant<int, 2>{}, i + 2);
+            if (i + 3 < nk) step(std::integral_constant<int, 3>{}, i + 3);
         }
     }
     wait_vmcnt_le<0>();  // nothing may land in LDS after the workgroup has ended
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
+    for (int h = 0; h < FT; ++h)
 #pragma unroll
-        for (int h = 0; h < FT; ++h) base_store4<DT>(p, t0 + wt + 16 * h + lr, n0 + wn + 16 * f + 4 * lg, acc[f][h]);
+        for (int f = 0; f < FN; f += 2) {
+            const int t = t0 + wt + 16 * h + lr, n = n0 + wn + 16 * f + 8 * lg;
+            if (p.splits == 1)
+                base_store8<DT>(p, t, n, acc[f][h], acc[f + 1][h]);
+            else if (t < p.T && n < p.N) {
+                LORA_GLOBAL f32x4_t* d = gptr(reinterpret_cast<f32x4_t*>(p.part + ((int64_t)part * p.T + t) * p.N + n));
+                d[0] = acc[f][h];
+                d[1] = acc[f + 1][h];
+            }
+        }
+}
+
+// The sum of the parts of a split k, in order, as base_kernel stores it: a
+// thread takes four outputs of a row.
+constexpr int kSumThreads = 256;
+template <int DT>
+__global__ __launch_bounds__(kSumThreads) void base_sum_kernel(BaseParams p) {
+    const int64_t q = (int64_t)p.T * (p.N / 4);
+    for (int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; i < q; i += (int64_t)gridDim.x * kSumThreads) {
+        const LORA_GLOBAL f32x4_t* src = gptr(reinterpret_cast<const f32x4_t*>(p.part)) + i;
+        f32x4_t sum = src[0];
+        for (int s = 1; s < p.splits; ++s) sum += src[s * q];
+        const int64_t t = i / (p.N / 4);
+        base_store4<DT>(p, (int)t, 4 * (int)(i - t * (p.N / 4)), sum);
+    }
+}
+
+// ------------------------------------------------------------------ few rows: the weight as a stream
+//
+// Up to 16 FT rows: the weight is read once, straight into operand registers,
+// and nothing of it is shared between waves.  A workgroup of NW waves computes
+// 16 outputs of every row; wave w takes the blocks w, w + NW, ... along k (a
+// workgroup reads NW * 128 consecutive bytes of each of its 16 weight rows at a
+// time) and the waves' sums are added in wave order through LDS.  kU blocks a
+// wave are in flight at once.
+constexpr int kU = 4;
+
+template <int FT, int NW, int DT>
+__global__ __launch_bounds__(NW* kWave) void base_stream_kernel(BaseParams p) {
+    __shared__ f32x4_t s_acc[NW][FT][kWave];
+    const int wave = wave_id();
+    const int lane = threadIdx.x & (kWave - 1);
+    const int lr = lane & 15, lg = lane >> 4;
+    const int n0 = blockIdx.x * 16;
+    const LORA_GLOBAL uint8_t* w = gptr(p.w + (int64_t)min(n0 + lr, p.N - 1) * p.ldw + 16 * lg);
+    const uint8_t* ws = p.ws + (int64_t)(n0 / kQBlock) * p.ldws;
+    const LORA_GLOBAL uint8_t *x[FT], *xs[FT];
+#pragma unroll
+    for (int f = 0; f < FT; ++f) {
+        const int64_t t = min(16 * f + lr, p.T - 1);
+        x[f] = gptr(p.x + t * p.ldx + 16 * lg);
+        xs[f] = gptr(p.xs + t * p.ldxs);
+    }
+    f32x4_t acc[FT];
+#pragma unroll
+    for (int f = 0; f < FT; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int k0 = wave; k0 < p.nkb; k0 += NW * kU) {
+        QuantOperand a[kU], b[kU][FT];
+        uint32_t as[kU], bs[kU][FT];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int kb = min(k0 + NW * u, p.nkb - 1);
+            const int off = kb * kQBlock;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                a[u].u[i] = __builtin_nontemporal_load(reinterpret_cast<const LORA_GLOBAL u32x4_t*>(w + off + 64 * i));
+            as[u] = cptr(ws)[kb];
+#pragma unroll
+            for (int f = 0; f < FT; ++f) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    b[u][f].u[i] = *reinterpret_cast<const LORA_GLOBAL u32x4_t*>(x[f] + off + 64 * i);
+                bs[u][f] = xs[f][kb];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            if (k0 + NW * u < p.nkb) {
+                const QuantFrag<DT> af = QuantFrag<DT>::template make<0>(a[u], as[u]);
+#pragma unroll
+                for (int f = 0; f < FT; ++f)
+                    acc[f] = af.template mma<0>(QuantFrag<DT>::template make<0>(b[u][f], bs[u][f]), acc[f]);
+            }
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < FT; ++f) s_acc[wave][f][lane] = acc[f];
+    __syncthreads();
+    if (wave < FT) {
+        f32x4_t sum = s_acc[0][wave][lane];
+#pragma unroll
+        for (int v = 1; v < NW; ++v) sum += s_acc[v][wave][lane];
+        base_store4<DT>(p, 16 * wave + lr, n0 + 4 * lg, sum);
+    }
 }
 
 }  // namespace lora

@@ -1,5 +1,22 @@
 // base.hip -- lora_base_product entry point.
+//
+// Which kernel, tile and split of k a call takes goes by a model of its time.
+// A tile kernel's workgroups take rounds of one per CU, a round its steps along
+// k; small tiles fill the chip, large ones load less per product.  Measured
+// (us, bf16 y; rows x k x outputs):
+//                     32x64  64x64  64x128 128x128 256x128 256x256
+//    256 x  4096 x 4096  17.8    8.9    11.2    15.6    22.3    39.3
+//   1024 x  4096 x 4096  49.8   27.2    23.4    17.9    24.1    41.3
+//   2048 x  4096 x 4096  98.1   51.9    45.5    34.3    29.8    42.3
+//   6783 x 4096 x 14336     -    596     522     414     348     302
+// Where the tiles leave CUs without work, k is split, for a second kernel that
+// adds the parts: 64 x 14336 x 4096, 64x64: 36.8 us in one part, 18.4 in four.
+// Up to 16 rows may take the weight as a stream instead: 1 x 4096 x 4096 5.8 us
+// against 8.8 for the best tiles, but 1 x 4096 x 14336 14.7 against 13.3 and
+// 16 x 14336 x 4096 21.6 against 15.1 (weights from HBM).
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "base.h"
 
@@ -7,17 +24,82 @@ using namespace lora;
 
 namespace {
 
-template <int BN, int BT, int WN, int WT, int ST>
-int launch_base(int dtype, BaseParams p, hipStream_t st) {
-    p.tiles_n = (p.N + BN - 1) / BN;
-    p.tiles_t = (p.T + BT - 1) / BT;
-    const int64_t tiles = (int64_t)p.tiles_n * p.tiles_t;
-    if (tiles > INT32_MAX - 8) return LORA_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)round_up(tiles, kNumXcd)), block(WN * WT * kWave);
-    if (dtype == LORA_BF16)
-        hipLaunchKernelGGL((base_kernel<BN, BT, WN, WT, ST, LORA_BF16>), grid, block, 0, st, p);
-    else
-        hipLaunchKernelGGL((base_kernel<BN, BT, WN, WT, ST, LORA_F32>), grid, block, 0, st, p);
+constexpr int kCus = 256;
+enum { kStream = 0, kTile32x64, kTile64x64, kTile64x128, kTile128x128, kTile256x128, kTile256x256, kKinds };
+struct BaseTile {
+    int bn, bt;
+    float start, step;  // us of a workgroup: its start and end, a step along k
+};
+constexpr BaseTile kTiles[kKinds] = {{0, 0, 0.f, 0.f},          {32, 64, 1.0f, 0.155f},   {64, 64, 1.0f, 0.17f},
+                                     {64, 128, 1.5f, 0.29f},    {128, 128, 2.5f, 0.45f},  {256, 128, 3.5f, 0.80f},
+                                     {256, 256, 6.0f, 1.38f}};
+constexpr int kStreamRows = 16;
+constexpr int kStreamWaves = 8;
+
+struct BasePlan {
+    int kind;
+    int32_t splits;
+};
+
+BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
+    const int64_t nkb = (k + kQBlock - 1) / kQBlock, groups = (nkb + 3) / 4;
+    const float rate = dtype == LORA_BF16 ? 1.f : 1.8f;  // fp32 y: four bf16 instructions a block
+    BasePlan best{kTile64x64, 1};
+    float least = 0.f;
+    for (int kind = kTile32x64; kind < kKinds; ++kind) {
+        const BaseTile& c = kTiles[kind];
+        const int64_t tiles = ((N + c.bn - 1) / c.bn) * ((T + c.bt - 1) / c.bt);
+        // in one part, or in as many as there are CUs for, or a half, a quarter, ... of that
+        for (int64_t s = std::max<int64_t>(1, std::min(groups, kCus / tiles)); s >= 1; s /= 2) {
+            const int64_t rounds = (tiles * s + kCus - 1) / kCus;
+            const float steps = 4.f * (float)((groups + s - 1) / s);
+            float us = (float)rounds * (c.start + std::min(steps, (float)nkb) * c.step * rate);
+            if (s > 1) us += 4.f + (float)s * (float)(T * N) * 8.f / 8e6f;
+            if (least == 0.f || us < least) {
+                least = us;
+                best = BasePlan{kind, (int32_t)s};
+            }
+        }
+    }
+    if (T <= kStreamRows && (float)(N * k) / 4.6e6f * (1.f + 0.03f * (float)(T - 1)) < least) best = BasePlan{kStream, 1};
+    return best;
+}
+
+int64_t part_bytes(const BasePlan& b, int64_t T, int64_t N) { return b.splits > 1 ? (int64_t)b.splits * T * N * 4 : 0; }
+
+template <int DT, int BN, int BT, int WN, int WT, int ST>
+void launch_tiles(const BaseParams& p, unsigned grid, hipStream_t st) {
+    hipLaunchKernelGGL((base_kernel<BN, BT, WN, WT, ST, DT>), dim3(grid), dim3(WN * WT * kWave), 0, st, p);
+}
+
+template <int DT>
+int launch_base(BaseParams p, const BasePlan& b, hipStream_t st) {
+    p.splits = b.splits;
+    if (b.kind == kStream) {
+        hipLaunchKernelGGL((base_stream_kernel<kStreamRows / 16, kStreamWaves, DT>), dim3((unsigned)((p.N + 15) / 16)),
+                           dim3(kStreamWaves * kWave), 0, st, p);
+        return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+    }
+    const BaseTile& c = kTiles[b.kind];
+    p.tiles_n = (p.N + c.bn - 1) / c.bn;
+    p.tiles_t = (p.T + c.bt - 1) / c.bt;
+    const int64_t tasks = (int64_t)p.tiles_n * p.tiles_t * p.splits;
+    if (tasks > INT32_MAX - kNumXcd * kBand) return LORA_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)round_up(tasks, kNumXcd);
+    switch (b.kind) {
+        case kTile32x64: launch_tiles<DT, 32, 64, 1, 4, 6>(p, grid, st); break;
+        case kTile64x64: launch_tiles<DT, 64, 64, 2, 2, 4>(p, grid, st); break;
+        case kTile64x128: launch_tiles<DT, 64, 128, 2, 2, 4>(p, grid, st); break;
+        case kTile128x128: launch_tiles<DT, 128, 128, 2, 2, 3>(p, grid, st); break;
+        case kTile256x128: launch_tiles<DT, 256, 128, 2, 2, 2>(p, grid, st); break;
+        default: launch_tiles<DT, 256, 256, 2, 2, 2>(p, grid, st); break;
+    }
+    if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
+    if (p.splits > 1) {
+        const int64_t q = (int64_t)p.T * (p.N / 4);
+        const unsigned sum_grid = (unsigned)std::min<int64_t>((q + kSumThreads - 1) / kSumThreads, kCus * 8);
+        hipLaunchKernelGGL(base_sum_kernel<DT>, dim3(sum_grid), dim3(kSumThreads), 0, st, p);
+    }
     return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
@@ -25,7 +107,9 @@ int launch_base(int dtype, BaseParams p, hipStream_t st) {
 
 extern "C" size_t lora_base_product_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out) {
     if (T < 0 || d_in < 1 || d_out < 1) return 0;
-    return 16;
+    const int64_t need = std::max(part_bytes(base_plan(LORA_BF16, T, d_in, d_out), T, d_out),
+                                  part_bytes(base_plan(LORA_F32, T, d_in, d_out), T, d_out));
+    return (size_t)std::max<int64_t>(need, 16);
 }
 
 extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
@@ -55,5 +139,8 @@ extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_i
     p.N = d_out;
     p.nkb = (d_in + kQBlock - 1) / kQBlock;
     p.accumulate = accumulate;
-    return launch_base<64, 64, 2, 2, 4>(dtype, p, static_cast<hipStream_t>(stream));
+    p.part = static_cast<float*>(ws);
+    const BasePlan b = base_plan(dtype, T, d_in, d_out);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return dtype == LORA_BF16 ? launch_base<LORA_BF16>(p, b, st) : launch_base<LORA_F32>(p, b, st);
 }

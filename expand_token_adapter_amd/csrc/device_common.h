@@ -350,6 +350,17 @@ __device__ __forceinline__ void lds_dma16_async(const void* src, void* lds_row) 
         : "memory", "m0");
 }
 
+// lds_dma16_async with 4 bytes per lane (lane L's land at lds_row + 4 L).
+__device__ __forceinline__ void lds_dma4_async(const void* src, void* lds_row) {
+    const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds_row;
+    asm volatile(
+        "s_mov_b32 m0, %0\n\t"
+        "global_load_lds_dword %1, off"
+        :
+        : "s"(m0), "v"(src)
+        : "memory", "m0");
+}
+
 // Buffer resources (raw, untyped): loads through them take a 32-bit byte
 // offset from a wave-uniform base, and the hardware returns zeros for bytes at
 // or past num_records instead of touching memory there.
