@@ -543,8 +543,8 @@ def _backward(fn, x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, extra)
     lib = _abi.load()
     code = _dtype_code(dy if quant else x)
     if ws is None:  # a caller's workspace is size-checked by the library (LORA_ERR_WORKSPACE)
-        ws = torch.empty(max(lib.lora_backward_workspace_bytes(code, T, d_in, d_out, r_max), 1),
-                         dtype=torch.uint8, device=x.device)
+        query = lib.lora_backward_quant_workspace_bytes if quant else lib.lora_backward_workspace_bytes
+        ws = torch.empty(max(query(code, T, d_in, d_out, r_max), 1), dtype=torch.uint8, device=x.device)
     with _on_device(x.device):
         st = getattr(lib, fn)(code, *rows, pdy, lddy, pdx or None, lddx, T, d_in, d_out, adapters.ptr,
                               grads.ptr, len(adapters), r_max, seg_ft.c, pvs or None, ldv, ws.data_ptr(), ws.numel(),

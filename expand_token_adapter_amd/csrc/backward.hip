@@ -30,6 +30,7 @@
 #include "shrink.h"
 #include "expand.h"
 #include "contract.h"
+#include "contract_wide.h"
 #include "bwd_stream.h"
 
 using namespace lora;
@@ -37,6 +38,8 @@ using namespace lora;
 namespace lora {
 int run_shrink(int dtype, bool trans_w, const ShrinkParams& p, const ReduceParams& rp, int32_t T, int32_t num_adapters,
                hipStream_t st);
+int run_shrink_pair(int dtype, const ShrinkParams& g, const ReduceParams& gr, const ShrinkParams& v,
+                    const ReduceParams& vr, int32_t T, int32_t num_adapters, hipStream_t st);
 int64_t shrink_part_ld(int32_t r_max);
 int64_t shrink_part_floats(int dtype, int32_t T, int32_t K, int32_t r_max);
 int expand_plan(const ExpandParams& p, int32_t T, int32_t num_adapters, int32_t r_max, ExpandParams* q,
@@ -50,16 +53,22 @@ int launch_shrink_reduce(int32_t r_max, const ReduceParams& rp, int32_t T, int32
 constexpr int kXsideCtrGrid = LORA_XSIDE_CTR;
 static_assert(kXsideCtrGrid % kNumXcd == 0, "whole rounds of the 8 XCDs");
 
+// Saved 8-bit rows and adapters of rank above 16 take the wide contraction: 2048
+// rows of ranks 8 to 64, 4096 -> 14336: 37 us for the launch and 13 for its fix-up,
+// against 69 and 5.  At rank 16 the two read alike, and
+// contract.h's tiles, cut finer, leave smaller partial tiles.
+constexpr bool use_wide(bool quant, int64_t r_max) { return quant && r_max > 16; }
+
 // Workspace layout of lora_backward (fp32 elements): g by sorted position
 // (row-major and rank-major), v rank-major (two-pass path) or by sorted
 // position (streaming path, recomputed v), the split-K partials of the shrinks
 // or the streaming path's g partials (reused by the passes, which run one
-// after the other), and the partial tiles of the stream-K kernels.
+// after the other; a second set where g's and v's shrink run together), and the partial tiles of the stream-K kernels.
 struct BwdWs {
     int64_t ldg, ldT;               // pitch of g rows; pitch of the rank-major arrays
-    int64_t g, gT, vT, vpos, part, fix, fix_meta, dyfix, dymeta, total; // offsets
+    int64_t g, gT, vT, vpos, part, part2, fix, fix_meta, dyfix, dymeta, total; // offsets
     static int32_t dy_slices(int64_t d_out) { return (int32_t)((d_out + kDyCols - 1) / kDyCols); }
-    static BwdWs make(int dtype, int64_t T, int64_t d_in, int64_t d_out, int64_t r_max) {
+    static BwdWs make(int dtype, int64_t T, int64_t d_in, int64_t d_out, int64_t r_max, bool quant) {
         BwdWs w;
         w.ldg = round_up(r_max, 8);
         w.ldT = round_up(T > 0 ? T : 1, 32);
@@ -71,8 +80,10 @@ struct BwdWs {
         int64_t np = std::max(shrink_part_floats(dtype, (int32_t)T, (int32_t)d_in, (int32_t)r_max),
                               shrink_part_floats(dtype, (int32_t)T, (int32_t)d_out, (int32_t)r_max));
         np = std::max(np, (int64_t)dy_slices(d_out) * (T > 0 ? T : 1) * 16);
-        w.fix = round_up(w.part + np, 64);
-        w.fix_meta = w.fix + (int64_t)kXsideCtrGrid * 2 * kFixFloats;
+        w.part2 = round_up(w.part + np, 64);
+        w.fix = round_up(w.part2 + shrink_part_floats(dtype, (int32_t)T, (int32_t)d_in, (int32_t)r_max), 64);
+        const int64_t fix = use_wide(quant, r_max) ? wide_fix_floats(r_max <= 32 ? 2 : 4) : kFixFloats;
+        w.fix_meta = w.fix + (int64_t)kXsideCtrGrid * 2 * fix;
         w.dyfix = round_up(w.fix_meta + (int64_t)kXsideCtrGrid * 2 * kFixMeta, 64);
         w.dymeta = w.dyfix + (int64_t)kStGrid * 2 * kDyFixFloats;
         w.total = round_up(w.dymeta + (int64_t)kStGrid * 2 * kStFixMeta, 64);
@@ -105,6 +116,40 @@ void xside_kernel(ContractParams cp, int n_ctr, ExpandParams ep, int n_expand, D
         dy_fixup_body(dp, b - n_ctr - n_expand);
 }
 
+// The same for saved 8-bit rows and adapters of rank above 16 (contract_wide.h).
+template <int DT, int KS, int MB>
+__global__ __launch_bounds__(4 * kWave) __attribute__((amdgpu_waves_per_eu(DT == LORA_F32 ? 1 : 2)))
+void xside_wide_kernel(ContractParams cp, int n_ctr, ExpandParams ep, int n_expand) {
+    constexpr int kC = WideLds<DT, MB>::kBytes, kE = ExpandLds<KS>::kBytes;
+    __shared__ __attribute__((aligned(16))) char s_lds[kC > kE ? kC : kE];
+    const int b = (int)blockIdx.x;
+    if (b < n_ctr)
+        contract_wide_body<DT, MB>(cp, b, n_ctr, s_lds);
+    else
+        expand_body<DT, true, KS>(ep, b - n_ctr, n_expand, s_lds);
+}
+
+template <int DT, int KS, int MB>
+void launch_xside_wide(const ContractParams& cp, const ExpandParams& ep, unsigned n_expand, hipStream_t st) {
+    hipLaunchKernelGGL((xside_wide_kernel<DT, KS, MB>), dim3(kXsideCtrGrid + n_expand), dim3(4 * kWave), 0, st, cp,
+                       kXsideCtrGrid, ep, (int)n_expand);
+    hipLaunchKernelGGL(contract_wide_fixup_kernel<MB>, dim3(kXsideCtrGrid, 4), dim3(4 * kWave), 0, st, cp,
+                       (int)kXsideCtrGrid);
+}
+
+template <int DT>
+int run_xside_wide(ContractParams cp, const ExpandParams& ep, int32_t r_max, unsigned n_expand, hipStream_t st) {
+    cp.ncb_in = (cp.d_in + kWideCols - 1) / kWideCols;
+    cp.ncb_out = (cp.d_out + kWideCols - 1) / kWideCols;
+    if (r_max <= 32)
+        launch_xside_wide<DT, 1, 2>(cp, ep, n_expand, st);
+    else if (r_max <= 64)
+        launch_xside_wide<DT, 2, 4>(cp, ep, n_expand, st);
+    else
+        launch_xside_wide<DT, 4, 4>(cp, ep, n_expand, st);
+    return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
 template <int DT, bool NT, bool XQ>
 void launch_xside_q(int ks, const ContractParams& cp, const ExpandParams& ep, const DyParams& dp, unsigned n_expand,
                     unsigned n_dy, hipStream_t st) {
@@ -129,7 +174,7 @@ void launch_xside(int ks, const ContractParams& cp, const ExpandParams& ep, cons
 
 extern "C" size_t lora_backward_workspace_bytes(int dtype, int32_t T_ft, int32_t d_in, int32_t d_out, int32_t r_max) {
     if (!valid_dtype(dtype) || T_ft < 0 || d_in < 1 || d_out < 1 || r_max < 1 || r_max > LORA_MAX_RANK) return 0;
-    return (size_t)BwdWs::make(dtype, T_ft, d_in, d_out, r_max).total * sizeof(float);
+    return (size_t)BwdWs::make(dtype, T_ft, d_in, d_out, r_max, false).total * sizeof(float);
 }
 
 namespace {
@@ -175,7 +220,7 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const lora_quant* xq, c
     if (dx && (rc = check_matrix(dx, d_in, lddx)) != LORA_OK) return rc;
     if (v_saved && (rc = check_f32_rows(v_saved, ldv, r_max)) != LORA_OK) return rc;
     if (!seg_ft.offsets) return LORA_ERR_INVALID_ARG;
-    const BwdWs w = BwdWs::make(dtype, T_ft, d_in, d_out, r_max);
+    const BwdWs w = BwdWs::make(dtype, T_ft, d_in, d_out, r_max, xq != nullptr);
     if (!ws || !aligned16(ws) || ws_bytes < (size_t)w.total * sizeof(float)) return LORA_ERR_WORKSPACE;
 
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -222,21 +267,28 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const lora_quant* xq, c
     rp.stop = stop;
 
     // v = A x when the caller did not save it: by sorted position for the
-    // one-pass kernel, rank-major for the contraction.
+    // one-pass kernel, rank-major for the contraction.  Where nothing has to
+    // stand between the two, it shares its launches with g's below.
+    ShrinkParams vp = sp;
+    ReduceParams vr = rp;
+    const bool pair = !v_saved && !one_pass && !grant;
     if (!v_saved) {
-        ShrinkParams vp = sp;
         vp.x = xq ? xq->codes : x;
         vp.ldx = xq ? xq->ld : ldx;
         vp.xs = xq ? xq->scales : nullptr;
         vp.ldxs = xq ? xq->lds : 0;
         vp.K = d_in;
         vp.nslices = shrink_slices(dtype, d_in);
-        ReduceParams vr = rp;
         vr.nslices = vp.nslices;
         vr.out = one_pass ? vpos : nullptr;
         vr.ldo = w.ldg;
         vr.outT = one_pass ? nullptr : vT;
-        if ((rc = run_shrink(dtype, false, vp, vr, T_ft, num_adapters, st)) != LORA_OK) return rc;
+        if (pair) {
+            vp.part = wsf + w.part2;
+            vr.part = vp.part;
+        } else if ((rc = run_shrink(dtype, false, vp, vr, T_ft, num_adapters, st)) != LORA_OK) {
+            return rc;
+        }
         if (grant) {
             hipLaunchKernelGGL(bwd_gate_kernel, dim3(1), dim3(kWave), 0, st, grant, status, 0);
             if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
@@ -298,7 +350,9 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const lora_quant* xq, c
             gr.ldvsrc = ldv;
             gr.vT = vT;
         }
-        if ((rc = run_shrink(dtype, true, gp, gr, T_ft, num_adapters, st)) != LORA_OK) return rc;
+        rc = pair ? run_shrink_pair(dtype, gp, gr, vp, vr, T_ft, num_adapters, st)
+                  : run_shrink(dtype, true, gp, gr, T_ft, num_adapters, st);
+        if (rc != LORA_OK) return rc;
     }
 
     // dA += s g^T x (and, on the two-pass path, dB += s dy^T v).
@@ -350,6 +404,9 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const lora_quant* xq, c
         ep.stop = stop;
         ks = expand_plan(ep, T_ft, num_adapters, r_max, &q, &n_expand);
     }
+    if (use_wide(xq != nullptr, r_max))
+        return dtype == LORA_BF16 ? run_xside_wide<LORA_BF16>(cp, q, r_max, n_expand, st)
+                                  : run_xside_wide<LORA_F32>(cp, q, r_max, n_expand, st);
     if (dtype == LORA_BF16 && !one_pass)
         launch_xside<LORA_BF16, true>(ks, cp, q, dp, n_expand, n_dy, st);
     else if (dtype == LORA_BF16)
@@ -385,7 +442,8 @@ extern "C" int lora_backward_preemptible(int dtype, const void* x, int64_t ldx, 
 
 extern "C" size_t lora_backward_quant_workspace_bytes(int dtype, int32_t T_ft, int32_t d_in, int32_t d_out,
                                                       int32_t r_max) {
-    return lora_backward_workspace_bytes(dtype, T_ft, d_in, d_out, r_max);
+    if (lora_backward_workspace_bytes(dtype, T_ft, d_in, d_out, r_max) == 0) return 0;
+    return (size_t)BwdWs::make(dtype, T_ft, d_in, d_out, r_max, true).total * sizeof(float);
 }
 
 extern "C" int lora_backward_quant(int dtype, lora_quant x, const void* dy, int64_t lddy, void* dx, int64_t lddx,

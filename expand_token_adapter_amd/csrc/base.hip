@@ -107,6 +107,7 @@ int launch_base(BaseParams p, const BasePlan& b, hipStream_t st) {
 
 extern "C" size_t lora_base_product_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out) {
     if (T < 0 || d_in < 1 || d_out < 1) return 0;
+    if (T == 0) return 16;
     const int64_t need = std::max(part_bytes(base_plan(LORA_BF16, T, d_in, d_out), T, d_out),
                                   part_bytes(base_plan(LORA_F32, T, d_in, d_out), T, d_out));
     return (size_t)std::max<int64_t>(need, 16);

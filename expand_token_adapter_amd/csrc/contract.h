@@ -149,25 +149,34 @@ __device__ __forceinline__ void contract_rows(int32_t* rows, const int32_t* perm
     }
 }
 
+// The Q part of a window: 4 rows x 8 columns from col.  NT: loaded with the
+// nontemporal hint.
+template <int DT, bool NT, bool Q8>
+__device__ __forceinline__ void contract_load_q(std::conditional_t<Q8, QuantRaw, Frag<DT>>* w, const char* q,
+                                                int64_t ldq, const uint8_t* qs, int64_t ldqs, const int32_t* rows,
+                                                int col) {
+    constexpr int EB = Frag<DT>::kBytes;
+    if constexpr (Q8) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = QuantRaw::load(reinterpret_cast<const uint8_t*>(q) + rows[j] * ldq, qs + rows[j] * ldqs, col);
+    } else if constexpr (NT && DT == LORA_BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j].q = __builtin_nontemporal_load(
+                gptr(reinterpret_cast<const u32x4_t*>(q + ((int64_t)rows[j] * ldq + col) * EB)));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = Frag<DT>::load(q + ((int64_t)rows[j] * ldq + col) * EB);
+    }
+}
+
 // NT: the window's x / dY rows are loaded with the nontemporal hint.
 template <int DT, bool NT, bool Q8>
 __device__ __forceinline__ void contract_load(ContractWin<DT, Q8>& W, const char* q, int64_t ldq, const uint8_t* qs,
                                               int64_t ldqs, const float* PT, int64_t ldT, const int32_t* rows, int win,
                                               int c0, int lcol, int rank0, int r, int lane) {
-    constexpr int EB = Frag<DT>::kBytes;
-    if constexpr (Q8) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            W.q[j] = QuantRaw::load(reinterpret_cast<const uint8_t*>(q) + rows[j] * ldq, qs + rows[j] * ldqs, c0 + lcol);
-    } else if constexpr (NT && DT == LORA_BF16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            W.q[j].q = __builtin_nontemporal_load(
-                gptr(reinterpret_cast<const u32x4_t*>(q + ((int64_t)rows[j] * ldq + c0 + lcol) * EB)));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) W.q[j] = Frag<DT>::load(q + ((int64_t)rows[j] * ldq + c0 + lcol) * EB);
-    }
+    contract_load_q<DT, NT, Q8>(W.q, q, ldq, qs, ldqs, rows, c0 + lcol);
     const int pp = win + 8 * (lane >> 4);
 #pragma unroll
     for (int mb = 0; mb < kContractMB; ++mb) {
@@ -178,26 +187,32 @@ __device__ __forceinline__ void contract_load(ContractWin<DT, Q8>& W, const char
     }
 }
 
+// Q tile -> LDS.
 template <int DT, bool Q8>
-__device__ __forceinline__ void contract_compute(const ContractWin<DT, Q8>& W, char* tile, f32x4_t (*acc)[4], int win,
-                                                 int lo, int hi, int lcol, int lrow, int nmb, int lane) {
-    using F = Frag<DT>;
-    const int lr = lane & 15;
-    const int lg = lane >> 4;
-    // 1. Q tile -> LDS;  2. B operands: column 16 nb + lr, window rows 8 lg .. 8 lg + 7.
-    F qf[4];
-    F raw[4];
+__device__ __forceinline__ void contract_tile_write(const std::conditional_t<Q8, QuantRaw, Frag<DT>>* w, char* tile,
+                                                    int lcol, int lrow) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+        Frag<DT> raw;
         if constexpr (Q8)
-            raw[j] = W.q[j].template frag<DT>();
+            raw = w[j].template frag<DT>();
         else
-            raw[j] = W.q[j];
-    }
-    if constexpr (DT == LORA_BF16) {
-        uint16_t* t = reinterpret_cast<uint16_t*>(tile);
+            raw = w[j];
+        if constexpr (DT == LORA_BF16) {
+            *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(tile) + (lrow + j) * kQPitch + lcol) = raw.q;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) *reinterpret_cast<u32x4_t*>(t + (lrow + j) * kQPitch + lcol) = raw[j].q;
+            for (int e = 0; e < 8; ++e) reinterpret_cast<float*>(tile)[(lcol + e) * kCtPitch + lrow + j] = raw.get(e);
+        }
+    }
+}
+// B operands of the tile: column 16 nb + lr, window rows 8 lg .. 8 lg + 7.
+template <int DT>
+__device__ __forceinline__ void contract_tile_read(Frag<DT>* qf, const char* tile, int lane) {
+    const int lr = lane & 15;
+    const int lg = lane >> 4;
+    if constexpr (DT == LORA_BF16) {
+        const uint16_t* t = reinterpret_cast<const uint16_t*>(tile);
         const int e = lr >> 2;
         const int c = lane & 3;
 #pragma unroll
@@ -208,14 +223,21 @@ __device__ __forceinline__ void contract_compute(const ContractWin<DT, Q8>& W, c
             qf[nb].q = u32x4_t{a.x, a.y, b.x, b.y};
         }
     } else {
-        float* t = reinterpret_cast<float*>(tile);
+        const float* t = reinterpret_cast<const float*>(tile);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[(lcol + e) * kCtPitch + lrow + j] = raw[j].get(e);
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) qf[nb] = F::load_lds(t + (16 * nb + lr) * kCtPitch + 8 * lg);
+        for (int nb = 0; nb < 4; ++nb) qf[nb] = Frag<DT>::load_lds(t + (16 * nb + lr) * kCtPitch + 8 * lg);
     }
+}
+
+template <int DT, bool Q8>
+__device__ __forceinline__ void contract_compute(const ContractWin<DT, Q8>& W, char* tile, f32x4_t (*acc)[4], int win,
+                                                 int lo, int hi, int lcol, int lrow, int nmb, int lane) {
+    using F = Frag<DT>;
+    const int lr = lane & 15;
+    const int lg = lane >> 4;
+    F qf[4];
+    contract_tile_write<DT, Q8>(W.q, tile, lcol, lrow);
+    contract_tile_read<DT>(qf, tile, lane);
     // 3. A operands from P^T (zero outside [lo, hi)), hi/lo split for bf16.
     const int pp = win + 8 * lg;
 #pragma unroll

@@ -108,9 +108,10 @@ __device__ __forceinline__ void shrink_slice_mma(f32x4_t* acc, const X (*xr)[2],
 // RB: 16-rank blocks a task covers (1, 2 or 4, from r_max): the weight slice
 // in LDS (16 RB rank rows of 1 KB) and the accumulators are sized for it, so
 // small ranks leave room for more workgroups per CU.  XQ: x is saved 8-bit rows.
+// (as workgroup blk of nblk, nblk a multiple of 8, the workgroup at a launch
+// index congruent to blk modulo 8; s_w: 16 RB rank rows of LDS)
 template <int DT, bool TRANS_W, int RB, bool XQ>
-__global__ __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4)))
-void shrink_kernel(ShrinkParams p) {
+__device__ __forceinline__ void shrink_body(const ShrinkParams& p, int blk, int nblk, u32x4_t* s_w) {
     using F = Frag<DT>;
     constexpr int EB = F::kBytes;
     constexpr int EPU = 16 / EB;                 // elements per 16-byte unit
@@ -119,7 +120,6 @@ void shrink_kernel(ShrinkParams p) {
     static_assert(RB == 1 || RB == 2 || RB == 4, "rank blocks per task");
     constexpr int NU = 16 * RB * 64 / kShrinkThreads; // row-major weight rows x units per thread
     constexpr int kTB = 4;                       // transposed weight units per thread and batch
-    __shared__ __attribute__((aligned(16))) u32x4_t s_w[16 * RB * 64];
     char* s_wb = reinterpret_cast<char*>(s_w);
     f32x4_t* s_red = reinterpret_cast<f32x4_t*>(s_w);  // reused after the MFMA pass
 
@@ -132,7 +132,7 @@ void shrink_kernel(ShrinkParams p) {
     const int kh = wave >> 2;  // half of the slice
     const int ntiles = p.sched[1];
     const int64_t n_tasks = (int64_t)ntiles * p.rgroups * p.nslices;
-    const TaskSlice ts = xcd_slice(n_tasks, 1, 0);
+    const TaskSlice ts = xcd_slice_of(blk, nblk, n_tasks, 1, 0);
     const int nkc = (p.K + 63) / 64;
 
     // Metadata of the next task (consecutive tasks: consecutive tiles of the
@@ -309,6 +309,26 @@ void shrink_kernel(ShrinkParams p) {
         }
         __syncthreads();  // the weight slice is rewritten by the next task
     }
+}
+
+template <int DT, bool TRANS_W, int RB, bool XQ>
+__global__ __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4)))
+void shrink_kernel(ShrinkParams p) {
+    __shared__ __attribute__((aligned(16))) u32x4_t s_w[16 * RB * 64];
+    shrink_body<DT, TRANS_W, RB, XQ>(p, blockIdx.x, gridDim.x, s_w);
+}
+
+// Two shrinks in one launch: g = B^T dy on the first n_g workgroups, v = A x on
+// the others (the backward without a saved v; neither needs the other).
+template <int DT, int RB, bool XQ>
+__global__ __launch_bounds__(kShrinkThreads) __attribute__((amdgpu_waves_per_eu(4)))
+void shrink_pair_kernel(ShrinkParams g, ShrinkParams v, int n_g) {
+    __shared__ __attribute__((aligned(16))) u32x4_t s_w[16 * RB * 64];
+    const int b = (int)blockIdx.x;
+    if (b < n_g)
+        shrink_body<DT, true, RB, false>(g, b, n_g, s_w);
+    else
+        shrink_body<DT, false, RB, XQ>(v, b - n_g, (int)gridDim.x - n_g, s_w);
 }
 
 // Sum of the K-slice partials, in slice order, for every row with an adapter:

@@ -108,8 +108,13 @@ def test_backward_refusals(lib):
 
 def test_queries(lib):
     assert lib.lora_base_product_workspace_bytes(-1, 8, 8) == 0 and lib.lora_base_product_workspace_bytes(1, 0, 8) == 0
-    assert lib.lora_base_product_workspace_bytes(1, 8, 0) == 0 and lib.lora_base_product_workspace_bytes(0, 8, 8) >= 0
+    assert lib.lora_base_product_workspace_bytes(1, 8, 0) == 0 and lib.lora_base_product_workspace_bytes(0, 8, 8) > 0
     assert lib.lora_backward_quant_workspace_bytes(0, -1, 8, 8, 8) == 0
+    # (parts of a split contraction: never more than a few tiles' worth for each CU)
+    for T in (1, 16, 17, 300, 5000, 2 ** 31 - 1):
+        for k in (8, 4096, 2 ** 22):
+            for n in (8, 1032, 2 ** 20):
+                assert 16 <= lib.lora_base_product_workspace_bytes(T, k, n) <= 256 * 256 * 256 * 4
 
 
 def test_binding_refuses():
