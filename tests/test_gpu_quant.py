@@ -156,6 +156,21 @@ SIZES = [(1, 8, 8), (1, 128, 16), (1, 4096, 264), (2, 136, 72), (15, 520, 136), 
 @pytest.mark.parametrize("add", [False, True])
 @pytest.mark.parametrize("T,k,n", SIZES)
 def test_base_product(T, k, n, add, dtype):
+    _check_product(T, k, n, add, dtype)
+
+
+# every tile and split: about a round of each tile on the chip, with ragged edges along all three sizes
+LARGE = [(12, 264, 14344), (40, 10248, 1032), (200, 12000, 264), (520, 520, 4104), (1030, 520, 4104), (2050, 776, 4104),
+         (4100, 392, 4104), (300, 33000, 136)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,k,n", LARGE)
+def test_base_product_large(T, k, n, dtype):
+    _check_product(T, k, n, T % 4 == 0, dtype)
+
+
+def _check_product(T, k, n, add, dtype):
     dt = TYPES[dtype]
     x, w, xv, wv = _product_case(T, k, n, T + k + n)
     y0 = torch.randn(T, n, generator=torch.Generator().manual_seed(9)).to(dt)
