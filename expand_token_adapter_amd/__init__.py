@@ -22,7 +22,6 @@ block of 128):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -71,9 +70,12 @@ def _on_gpu(*ts: Optional[torch.Tensor]) -> None:
 
 def _rows(t: torch.Tensor, name: str):
     """(pointer, rows, cols, pitch) of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.stride(1) != 1:
-        raise ValueError(f"{name} must be 2-D with contiguous rows")
-    return t.data_ptr(), t.shape[0], t.shape[1], t.stride(0)
+    if t.dim() == 2:
+        rows, cols = t.shape
+        pitch, step = t.stride()
+        if step == 1:
+            return t.data_ptr(), rows, cols, pitch
+    raise ValueError(f"{name} must be 2-D with contiguous rows")
 
 
 def _check_batch(name: str, adapters: "AdapterTable", seg: "Segments", T: int, *, x=None, y=None,
@@ -536,7 +538,7 @@ def _backward(fn, x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, extra)
     for i, (ga, gb) in enumerate(zip(grads.dA, grads.dB)):
         if ga is None:
             continue
-        if tuple(ga.shape) != tuple(adapters.A[i].shape) or tuple(gb.shape) != tuple(adapters.B[i].shape):
+        if ga.shape != adapters.A[i].shape or gb.shape != adapters.B[i].shape:
             raise ValueError(f"{fn}: gradient entry {i} must have the shapes of A[{i}] and B[{i}]")
         if ga.device != adapters.device or gb.device != adapters.device:
             raise ValueError(f"{fn}: gradient entry {i} is on another device")
@@ -545,32 +547,32 @@ def _backward(fn, x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, extra)
     if ws is None:  # a caller's workspace is size-checked by the library (LORA_ERR_WORKSPACE)
         query = lib.lora_backward_quant_workspace_bytes if quant else lib.lora_backward_workspace_bytes
         ws = torch.empty(max(query(code, T, d_in, d_out, r_max), 1), dtype=torch.uint8, device=x.device)
-    with _on_device(x.device):
-        st = getattr(lib, fn)(code, *rows, pdy, lddy, pdx or None, lddx, T, d_in, d_out, adapters.ptr,
-                              grads.ptr, len(adapters), r_max, seg_ft.c, pvs or None, ldv, ws.data_ptr(), ws.numel(),
-                              *extra, _stream(x.device))
+    st = _launch(x.device, getattr(lib, fn), code, *rows, pdy, lddy, pdx or None, lddx, T, d_in, d_out, adapters.ptr,
+                 grads.ptr, len(adapters), r_max, seg_ft.c, pvs or None, ldv, ws.data_ptr(), ws.numel(), *extra)
     _abi.check(fn, st)
 
 
-def _on_device(dev: torch.device):
-    """Makes dev the current device where it is not (kernels are launched on the current device)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(dev: torch.device, fn, *args) -> int:
+    """fn(*args, stream) on dev's current stream, with dev the current device (kernels are launched there)."""
+    if dev.index is None or dev.index == _device_index():
+        return fn(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream(dev))
 
 
 def lora_quant_rows(x: torch.Tensor, out: Optional[QuantRows] = None) -> QuantRows:
     """Save rows x [T, d] (bfloat16 or float32) in 8 bits; out: buffers to fill (QuantRows.empty, or a slice)."""
     _on_gpu(x)
-    code = _dtype_code(x)
+    code, dev = _dtype_code(x), x.device
     px, T, d, ldx = _rows(x, "x")
     if out is None:
-        out = QuantRows.empty(T, d, x.device)
-    elif out.T != T or out.d != d or out.device != x.device:
+        out = QuantRows.empty(T, d, dev)
+    elif out.T != T or out.d != d or out.device != dev:
         raise ValueError(f"out must hold {T} rows of {d} values on x's device")
-    with _on_device(x.device):
-        st = _abi.load().lora_quant_rows(code, px, ldx, T, d, out.c, _stream(x.device))
-    _abi.check("lora_quant_rows", st)
+    _abi.check("lora_quant_rows", _launch(dev, _abi.load().lora_quant_rows, code, px, ldx, T, d, out.c))
     return out
 
 
@@ -582,11 +584,10 @@ def lora_dequant_rows(q: QuantRows, dtype: torch.dtype = torch.bfloat16,
     _on_gpu(out)
     code = _dtype_code(out)
     px, T, d, ldx = _rows(out, "out")
-    if T != q.T or d != q.d or out.device != q.device:
+    dev = q.device
+    if T != q.T or d != q.d or out.device != dev:
         raise ValueError(f"out must be [{q.T}, {q.d}] on q's device")
-    with _on_device(q.device):
-        st = _abi.load().lora_dequant_rows(code, q.c, T, d, px, ldx, _stream(q.device))
-    _abi.check("lora_dequant_rows", st)
+    _abi.check("lora_dequant_rows", _launch(dev, _abi.load().lora_dequant_rows, code, q.c, T, d, px, ldx))
     return out
 
 
@@ -600,8 +601,7 @@ def lora_quant_weight(w: torch.Tensor, transpose: bool = False, out: Optional[Qu
         out = QuantWeight(*QuantWeight._buffers(rows, -(-rows // _abi.LORA_QUANT_BLOCK), cols, w.device), rows, cols)
     elif out.d_out != rows or out.d_in != cols or out.device != w.device:
         raise ValueError(f"out must be a [{rows}, {cols}] weight on w's device")
-    with _on_device(w.device):
-        st = _abi.load().lora_quant_weight(code, pw, ldw, d_out, d_in, int(bool(transpose)), out.c, _stream(w.device))
+    st = _launch(w.device, _abi.load().lora_quant_weight, code, pw, ldw, d_out, d_in, int(bool(transpose)), out.c)
     _abi.check("lora_quant_weight", st)
     return out
 
@@ -632,9 +632,8 @@ def lora_base_product(x: QuantRows, w: QuantWeight, y: Optional[torch.Tensor] = 
         ws = torch.empty(max(lib.lora_base_product_workspace_bytes(T, x.d, d_out), 1), dtype=torch.uint8, device=dev)
     elif ws.device != dev or not ws.is_contiguous():
         raise ValueError("ws must be contiguous on x's device")
-    with _on_device(dev):
-        st = lib.lora_base_product(code, x.c, T, x.d, w.c, d_out, py, ldy, int(bool(accumulate)), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(), _stream(dev))
+    st = _launch(dev, lib.lora_base_product, code, x.c, T, x.d, w.c, d_out, py, ldy, 1 if accumulate else 0,
+                 ws.data_ptr(), ws.nbytes)
     _abi.check("lora_base_product", st)
     return y
 

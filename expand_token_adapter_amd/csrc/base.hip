@@ -41,9 +41,9 @@ struct BasePlan {
     int32_t splits;
 };
 
-BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
+// (the same for both types of y: fp32 takes about twice as long on every tile)
+BasePlan base_plan(int64_t T, int64_t k, int64_t N) {
     const int64_t nkb = (k + kQBlock - 1) / kQBlock, groups = (nkb + 3) / 4;
-    const float rate = dtype == LORA_BF16 ? 1.f : 1.8f;  // fp32 y: four bf16 instructions a block
     BasePlan best{kTile64x64, 1};
     float least = 0.f;
     for (int kind = kTile32x64; kind < kKinds; ++kind) {
@@ -53,7 +53,7 @@ BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
         for (int64_t s = std::max<int64_t>(1, std::min(groups, kCus / tiles)); s >= 1; s /= 2) {
             const int64_t rounds = (tiles * s + kCus - 1) / kCus;
             const float steps = 4.f * (float)((groups + s - 1) / s);
-            float us = (float)rounds * (c.start + std::min(steps, (float)nkb) * c.step * rate);
+            float us = (float)rounds * (c.start + std::min(steps, (float)nkb) * c.step);
             if (s > 1) us += 4.f + (float)s * (float)(T * N) * 8.f / 8e6f;
             if (least == 0.f || us < least) {
                 least = us;
@@ -65,7 +65,9 @@ BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
     return best;
 }
 
-int64_t part_bytes(const BasePlan& b, int64_t T, int64_t N) { return b.splits > 1 ? (int64_t)b.splits * T * N * 4 : 0; }
+size_t workspace_bytes(const BasePlan& b, int64_t T, int64_t N) {
+    return b.splits > 1 ? (size_t)b.splits * (size_t)T * (size_t)N * sizeof(float) : 16;
+}
 
 template <int DT, int BN, int BT, int WN, int WT, int ST>
 void launch_tiles(const BaseParams& p, unsigned grid, hipStream_t st) {
@@ -107,10 +109,7 @@ int launch_base(BaseParams p, const BasePlan& b, hipStream_t st) {
 
 extern "C" size_t lora_base_product_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out) {
     if (T < 0 || d_in < 1 || d_out < 1) return 0;
-    if (T == 0) return 16;
-    const int64_t need = std::max(part_bytes(base_plan(LORA_BF16, T, d_in, d_out), T, d_out),
-                                  part_bytes(base_plan(LORA_F32, T, d_in, d_out), T, d_out));
-    return (size_t)std::max<int64_t>(need, 16);
+    return T == 0 ? 16 : workspace_bytes(base_plan(T, d_in, d_out), T, d_out);
 }
 
 extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
@@ -124,7 +123,8 @@ extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_i
     if (rc != LORA_OK) return rc;
     // a tile's 256 rows are addressed with 32-bit byte offsets
     if (x.ld > LORA_QUANT_MAX_LD || w.ld > LORA_QUANT_MAX_LD) return LORA_ERR_UNSUPPORTED;
-    if (!ws || !aligned16(ws) || ws_bytes < lora_base_product_workspace_bytes(T, d_in, d_out)) return LORA_ERR_WORKSPACE;
+    const BasePlan b = base_plan(T, d_in, d_out);
+    if (!ws || !aligned16(ws) || ws_bytes < workspace_bytes(b, T, d_out)) return LORA_ERR_WORKSPACE;
     BaseParams p{};
     p.x = x.codes;
     p.ldx = x.ld;
@@ -141,7 +141,6 @@ extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_i
     p.nkb = (d_in + kQBlock - 1) / kQBlock;
     p.accumulate = accumulate;
     p.part = static_cast<float*>(ws);
-    const BasePlan b = base_plan(dtype, T, d_in, d_out);
     hipStream_t st = static_cast<hipStream_t>(stream);
     return dtype == LORA_BF16 ? launch_base<LORA_BF16>(p, b, st) : launch_base<LORA_F32>(p, b, st);
 }
