@@ -29,21 +29,12 @@ __device__ __forceinline__ uint32_t quant_scale_byte(uint32_t top) {
     const int e = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
     return top == 0u ? 127u : (uint32_t)max(e, 0);
 }
-// 2^(127 - byte): the factor that takes a block's values to codes (bytes 0 .. 247).
-__device__ __forceinline__ float quant_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
 // The scale operand of gfx950's v_cvt_scalef32_* conversions: they take the
 // exponent field alone, so field 0 is 2^-127 and 255 is NaN, as the bytes are
 // (checked for every byte and code).
 __device__ __forceinline__ float quant_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 // ------------------------------------------------------------------ codes
-
-// 4 fp32 values (magnitude 448 or less) -> 4 codes, each rounded to nearest even.
-__device__ __forceinline__ uint32_t quant_codes4(float a, float b, float c, float d) {
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    w = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
-    return (uint32_t)w;
-}
 
 // 8 codes times a scale, as an operand fragment (bf16: exact for scale bytes
 // from 3 to 246, else rounded to nearest even).

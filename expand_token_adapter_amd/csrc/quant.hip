@@ -23,25 +23,64 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x121, 0xf, 0xf, true));
 }
 
-// Bits of the largest finite magnitude of 8 values.
-__device__ __forceinline__ uint32_t finite_max8(const float* f) {
+// fp32 bits of the largest magnitude of 8 values, at or above kNotFinite if one
+// of them is not finite.
+constexpr uint32_t kNotFinite = 0x7f800000u;
+__device__ __forceinline__ uint32_t max8(const Frag<LORA_BF16>& f) {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t top{0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2_t, f.q[i] & 0x7fff7fffu));
+    return (uint32_t)max(top[0], top[1]) << 16;
+}
+__device__ __forceinline__ uint32_t max8(const Frag<LORA_F32>& f) {
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t m = __float_as_uint(f[e]) & 0x7fffffffu;
-        top = max(top, m < 0x7f800000u ? m : 0u);
-    }
+    for (int i = 0; i < 4; ++i) top = max(top, max(f.q0[i] & 0x7fffffffu, f.q1[i] & 0x7fffffffu));
     return top;
 }
 
-// Codes of 8 values; what is not finite becomes NaN.
-__device__ __forceinline__ u32x2_t encode8(const float* f, uint32_t scale) {
-    const float inv = quant_inv_scale(scale);
-    float z[8];
+// The 8 values with zeros (nan false) or NaN in place of those that are not finite.
+template <int DT>
+__device__ Frag<DT> finite8(const Frag<DT>& f, bool nan) {
+    float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        z[e] = (__float_as_uint(f[e]) & 0x7f800000u) == 0x7f800000u ? __uint_as_float(0x7fc00000u) : f[e] * inv;
-    return u32x2_t{quant_codes4(z[0], z[1], z[2], z[3]), quant_codes4(z[4], z[5], z[6], z[7])};
+    for (int e = 0; e < 8; ++e) {
+        v[e] = f.get(e);
+        if ((__float_as_uint(v[e]) & kNotFinite) == kNotFinite) v[e] = nan ? __uint_as_float(0x7fc00000u) : 0.f;
+    }
+    return Frag<DT>::from_f32(v);
+}
+
+// Codes of 8 values with |value| <= 448 * 2^(scale - 127), or NaN.
+__device__ __forceinline__ u32x2_t encode8(const Frag<LORA_BF16>& f, uint32_t scale) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    typedef short i16x2_t __attribute__((ext_vector_type(2)));
+    const float s = quant_scale(scale);
+    u32x2_t c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = f.q[2 * i], hi = f.q[2 * i + 1];  // (a bit cast of a vector's element takes its first)
+        i16x2_t w{0, 0};
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(bf16x2_t, lo), s, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(w, __builtin_bit_cast(bf16x2_t, hi), s, true);
+        c[i] = __builtin_bit_cast(uint32_t, w);
+    }
+    return c;
+}
+__device__ __forceinline__ u32x2_t encode8(const Frag<LORA_F32>& f, uint32_t scale) {
+    typedef short i16x2_t __attribute__((ext_vector_type(2)));
+    const float s = quant_scale(scale);
+    u32x2_t c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        i16x2_t w{0, 0};
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, f.get(4 * i), f.get(4 * i + 1), s, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, f.get(4 * i + 2), f.get(4 * i + 3), s, true);
+        c[i] = __builtin_bit_cast(uint32_t, w);
+    }
+    return c;
 }
 
 struct RowsParams {
@@ -55,46 +94,76 @@ struct RowsParams {
     int32_t T, d, nb;  // nb: blocks of a row
 };
 
-// 16 lanes take one block of 128: 8 values (16 bytes of bf16) a lane, so a
-// wave reads 1 KB of bf16 in one load.  Columns past d are zeros.
+// 16 lanes take one block of 128, 8 values (16 bytes of bf16, 8 codes) a lane:
+// a wave's load is 1 KB of bf16 and its store 512 bytes of codes.  Each takes a
+// few blocks, all loads in flight at once.  Streams: 4096 x 5120 bf16 rows are
+// saved in 10.5 us (6.0 TB/s, 13.9 us from HBM; with 1 and 4 blocks 11.3 and
+// 11.0) and restored in 9.9 (with 1 and 2 blocks 11.1 and 10.2); a large copy runs
+// at 5.1 TB/s.  What bounds the save beside memory is vector work: the magnitudes
+// are compared as packed 16-bit integers and the conversion divides by the scale
+// (with fp32 arithmetic for both: 11.6 us).
+constexpr int kSaveUnits = 2, kRestoreUnits = 4;
+
+// Unit (row, block) i of this lane's 16; on: it exists.
+struct RowUnit {
+    int64_t row;
+    uint32_t blk;
+    int col;
+    bool on;
+};
+template <int U>
+__device__ __forceinline__ RowUnit row_unit(const RowsParams& p, int i) {
+    const uint32_t units = (uint32_t)p.T * (uint32_t)p.nb;
+    const uint32_t u = blockIdx.x * (uint32_t)(kThreads / 16 * U) + (uint32_t)(kThreads / 16 * i) + threadIdx.x / 16;
+    const uint32_t uc = u < units ? u : units - 1;
+    const uint32_t row = uc / (uint32_t)p.nb, blk = uc - row * (uint32_t)p.nb;
+    return RowUnit{(int64_t)row, blk, (int)blk * kQBlock + 8 * (int)(threadIdx.x & 15), u < units};
+}
+
+// (columns past d are zeros)
 template <int DT>
 __global__ __launch_bounds__(kThreads) void quant_rows_kernel(RowsParams p) {
     constexpr int EB = Frag<DT>::kBytes;
-    const int64_t units = (int64_t)p.T * p.nb;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 16);
-    const int sub = threadIdx.x & 15;
-    for (int64_t u0 = (int64_t)blockIdx.x * (kThreads / 16); u0 < units; u0 += step) {
-        const int64_t u = u0 + threadIdx.x / 16;
-        const bool on = u < units;  // (whole 16-lane rows go on or off together)
-        const int64_t row = (on ? u : 0) / p.nb;
-        const int blk = (int)((on ? u : 0) - row * p.nb);
-        const int col = blk * kQBlock + 8 * sub;
-        float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (on && col < p.d) Elem<DT>::load8(p.x + (row * p.ldx + col) * EB, f);
-        const uint32_t scale = quant_scale_byte(row16_max(finite_max8(f)));
-        const u32x2_t c = encode8(f, scale);
-        if (on) {
-            *gptr(reinterpret_cast<u32x2_t*>(p.codes + row * p.ld + col)) = c;
-            if (sub == 0) gptr(p.scales)[row * p.lds + blk] = (uint8_t)scale;
+    RowUnit r[kSaveUnits];
+    Frag<DT> f[kSaveUnits];
+#pragma unroll
+    for (int i = 0; i < kSaveUnits; ++i) {
+        r[i] = row_unit<kSaveUnits>(p, i);
+        f[i] = Frag<DT>::load(p.x + (r[i].row * p.ldx + (r[i].col < p.d ? r[i].col : 0)) * EB);
+    }
+#pragma unroll
+    for (int i = 0; i < kSaveUnits; ++i) {
+        f[i] = f[i].masked(r[i].col < p.d);
+        uint32_t top = row16_max(max8(f[i]));
+        if (__ballot(top >= kNotFinite)) {
+            // (rare: a block of this wave holds infinities or NaN)
+            top = row16_max(max8(finite8<DT>(f[i], false)));
+            f[i] = finite8<DT>(f[i], true);
+        }
+        const uint32_t scale = quant_scale_byte(top);
+        if (r[i].on) {
+            *gptr(reinterpret_cast<u32x2_t*>(p.codes + r[i].row * p.ld + r[i].col)) = encode8(f[i], scale);
+            if ((threadIdx.x & 15) == 0) gptr(p.scales)[r[i].row * p.lds + r[i].blk] = (uint8_t)scale;
         }
     }
 }
 
-// 16 lanes take one block of 128, 8 values a lane.
 template <int DT>
 __global__ __launch_bounds__(kThreads) void dequant_rows_kernel(RowsParams p) {
     constexpr int EB = Frag<DT>::kBytes;
-    const int64_t units = (int64_t)p.T * p.nb;
-    const int64_t step = (int64_t)gridDim.x * (kThreads / 16);
-    const int sub = threadIdx.x & 15;
-    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 16) + threadIdx.x / 16; u < units; u += step) {
-        const int64_t row = u / p.nb;
-        const int blk = (int)(u - row * p.nb);
-        const int col = blk * kQBlock + 8 * sub;
-        if (col >= p.d) continue;
-        const u32x2_t c = *gptr(reinterpret_cast<const u32x2_t*>(p.codes + row * p.ld + col));
-        store_frag(p.xo + (row * p.ldx + col) * EB, dequant8<DT>(c[0], c[1], quant_scale(gptr(p.scales)[row * p.lds + blk])));
+    RowUnit r[kRestoreUnits];
+    u32x2_t c[kRestoreUnits];
+    uint32_t s[kRestoreUnits];
+#pragma unroll
+    for (int i = 0; i < kRestoreUnits; ++i) {
+        r[i] = row_unit<kRestoreUnits>(p, i);
+        c[i] = *gptr(reinterpret_cast<const u32x2_t*>(p.codes + r[i].row * p.ld + r[i].col));
+        s[i] = gptr(p.scales)[r[i].row * p.lds + r[i].blk];
     }
+#pragma unroll
+    for (int i = 0; i < kRestoreUnits; ++i)
+        if (r[i].on && r[i].col < p.d)
+            store_frag(p.xo + (r[i].row * p.ldx + r[i].col) * EB, dequant8<DT>(c[i][0], c[i][1], quant_scale(s[i])));
 }
 
 struct WeightParams {
@@ -121,15 +190,14 @@ __global__ __launch_bounds__(kThreads) void quant_weight_kernel(WeightParams p) 
     const int r0 = threadIdx.x / 16;
     const int kb = blockIdx.x, nb = blockIdx.y;
     const int col = kb * kQBlock + 8 * sub;
-    float f[8][8];
+    Frag<DT> f[8];
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = nb * kQBlock + 16 * i + r0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
-        if (row < p.n && col < p.k) Elem<DT>::load8(p.w + ((int64_t)row * p.ldw + col) * EB, f[i]);
-        top = max(top, finite_max8(f[i]));
+        f[i] = Frag<DT>::zero();
+        if (row < p.n && col < p.k) f[i] = Frag<DT>::load(p.w + ((int64_t)row * p.ldw + col) * EB);
+        top = max(top, max8(finite8<DT>(f[i], false)));
     }
     top = row16_max(top);
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, kWave));
@@ -143,7 +211,7 @@ __global__ __launch_bounds__(kThreads) void quant_weight_kernel(WeightParams p) 
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = nb * kQBlock + 16 * i + r0;
-        const u32x2_t c = encode8(f[i], scale);
+        const u32x2_t c = encode8(finite8<DT>(f[i], true), scale);
         if constexpr (TR) {
             uint8_t* t = s_t + 8 * sub * kTrPitch + 16 * i + r0;
 #pragma unroll
@@ -164,15 +232,19 @@ __global__ __launch_bounds__(kThreads) void quant_weight_kernel(WeightParams p) 
     }
 }
 
-unsigned rows_grid(int64_t units) {
-    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((units + kThreads / 16 - 1) / (kThreads / 16), 256 * 32));
+unsigned rows_grid(const RowsParams& p, int units) {
+    const int64_t per = kThreads / 16 * units;
+    return (unsigned)(((int64_t)p.T * p.nb + per - 1) / per);
 }
 
 int check_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, const lora_quant& q) {
     if (!valid_dtype(dtype) || T < 0 || d < 1) return LORA_ERR_INVALID_ARG;
     if (T == 0) return LORA_OK;
-    const int rc = check_matrix(x, d, ldx);
-    return rc != LORA_OK ? rc : check_quant(q, d);
+    int rc = check_matrix(x, d, ldx);
+    if (rc == LORA_OK) rc = check_quant(q, d);
+    if (rc != LORA_OK) return rc;
+    // blocks are numbered in 32 bits
+    return (int64_t)T * ((d + (int64_t)kQBlock - 1) / kQBlock) > INT32_MAX ? LORA_ERR_UNSUPPORTED : LORA_OK;
 }
 
 RowsParams rows_params(int64_t ldx, int32_t T, int32_t d, const lora_quant& q) {
@@ -186,7 +258,7 @@ extern "C" int lora_quant_rows(int dtype, const void* x, int64_t ldx, int32_t T,
     if (rc != LORA_OK || T == 0) return rc;
     RowsParams p = rows_params(ldx, T, d, q);
     p.x = static_cast<const char*>(x);
-    const dim3 grid(rows_grid((int64_t)T * p.nb)), block(kThreads);
+    const dim3 grid(rows_grid(p, kSaveUnits)), block(kThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (dtype == LORA_BF16)
         hipLaunchKernelGGL(quant_rows_kernel<LORA_BF16>, grid, block, 0, st, p);
@@ -200,7 +272,7 @@ extern "C" int lora_dequant_rows(int dtype, lora_quant q, int32_t T, int32_t d, 
     if (rc != LORA_OK || T == 0) return rc;
     RowsParams p = rows_params(ldx, T, d, q);
     p.xo = static_cast<char*>(x);
-    const dim3 grid(rows_grid((int64_t)T * p.nb)), block(kThreads);
+    const dim3 grid(rows_grid(p, kRestoreUnits)), block(kThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (dtype == LORA_BF16)
         hipLaunchKernelGGL(dequant_rows_kernel<LORA_BF16>, grid, block, 0, st, p);

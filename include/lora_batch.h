@@ -464,7 +464,7 @@ typedef struct lora_quant {
 /*
  * Save rows: q = the 8-bit form of x [T, ldx] (dtype), d columns.  One kernel.
  * A range of a longer matrix is saved by pointer offsets of x and q (a row of
- * q is a row of codes and a row of scales).
+ * q is a row of codes and a row of scales).  LORA_ERR_UNSUPPORTED for 2^31 blocks or more.
  */
 int lora_quant_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, lora_quant q, void* stream);
 

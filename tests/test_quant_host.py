@@ -57,6 +57,7 @@ def test_rows_refusals(lib, fn):
     assert call(dtype=2) == BAD and call(T=-1) == BAD and call(d=0) == BAD
     assert call(x=None) == BAD and call(x=FAKE + 4) == BAD and call(ldx=192) == BAD
     assert call(d=196) == UNS and call(ldx=204) == UNS
+    assert call(T=2 ** 30) == UNS  # 2^31 blocks
     for kw, want in BAD_QUANT:
         assert call(q=_q(**kw)) == want, kw
 
