@@ -497,7 +497,8 @@ def lora_backward_quant(x: QuantRows, dy: torch.Tensor, adapters: AdapterTable, 
                         r_max: Optional[int] = None, ws: Optional[torch.Tensor] = None) -> None:
     """lora_backward from the fine-tuning rows' saved 8-bit layer input, read as it is.
 
-    dX, dA and dB (+=) equal those of lora_backward on lora_dequant_rows(x) bit for bit."""
+    The gradients (+=) are those of lora_backward on lora_dequant_rows(x): dX bit for bit, dA and dB
+    with g and v in full."""
     if not isinstance(x, QuantRows):
         raise TypeError("x must be a QuantRows (lora_quant_rows)")
     _backward("lora_backward_quant", x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, ())

@@ -53,11 +53,16 @@ int launch_shrink_reduce(int32_t r_max, const ReduceParams& rp, int32_t T, int32
 constexpr int kXsideCtrGrid = LORA_XSIDE_CTR;
 static_assert(kXsideCtrGrid % kNumXcd == 0, "whole rounds of the 8 XCDs");
 
-// Saved 8-bit rows and adapters of rank above 16 take the wide contraction: 2048
-// rows of ranks 8 to 64, 4096 -> 14336: 37 us for the launch and 13 for its fix-up,
-// against 69 and 5.  At rank 16 the two read alike, and
-// contract.h's tiles, cut finer, leave smaller partial tiles.
-constexpr bool use_wide(bool quant, int64_t r_max) { return quant && r_max > 16; }
+// Saved 8-bit rows and adapters of rank above 16 take the wide contraction where
+// its 256-column tiles give every workgroup more than 8 windows of 64 ranks:
+// below that its partial tiles cost more than the reads it saves.  us, wide
+// against contract.h's tiles, all adapters of one rank: 2048 rows, 4096 -> 14336,
+// rank 32 65 / 72, rank 64 90 / 120, rank 128 139 / 209; 4096 rows, 4096 -> 4096
+// rank 64 84 / 92; 2048 rows rank 64 62 / 57; 512 rows 52 / 35.
+constexpr int64_t wide_blocks(int64_t d) { return (d + kWideCols - 1) / kWideCols; }
+constexpr bool use_wide(bool quant, int64_t T, int64_t d_in, int64_t d_out, int64_t r_max) {
+    return quant && r_max > 16 && T * (wide_blocks(d_in) + wide_blocks(d_out)) * r_max > (int64_t)8 * 32 * 64 * kXsideCtrGrid;
+}
 
 // Workspace layout of lora_backward (fp32 elements): g by sorted position
 // (row-major and rank-major), v rank-major (two-pass path) or by sorted
@@ -82,7 +87,7 @@ struct BwdWs {
         np = std::max(np, (int64_t)dy_slices(d_out) * (T > 0 ? T : 1) * 16);
         w.part2 = round_up(w.part + np, 64);
         w.fix = round_up(w.part2 + shrink_part_floats(dtype, (int32_t)T, (int32_t)d_in, (int32_t)r_max), 64);
-        const int64_t fix = use_wide(quant, r_max) ? wide_fix_floats(r_max <= 32 ? 2 : 4) : kFixFloats;
+        const int64_t fix = use_wide(quant, T, d_in, d_out, r_max) ? wide_fix_floats(r_max <= 32 ? 2 : 4) : kFixFloats;
         w.fix_meta = w.fix + (int64_t)kXsideCtrGrid * 2 * fix;
         w.dyfix = round_up(w.fix_meta + (int64_t)kXsideCtrGrid * 2 * kFixMeta, 64);
         w.dymeta = w.dyfix + (int64_t)kStGrid * 2 * kDyFixFloats;
@@ -139,8 +144,8 @@ void launch_xside_wide(const ContractParams& cp, const ExpandParams& ep, unsigne
 
 template <int DT>
 int run_xside_wide(ContractParams cp, const ExpandParams& ep, int32_t r_max, unsigned n_expand, hipStream_t st) {
-    cp.ncb_in = (cp.d_in + kWideCols - 1) / kWideCols;
-    cp.ncb_out = (cp.d_out + kWideCols - 1) / kWideCols;
+    cp.ncb_in = (int32_t)wide_blocks(cp.d_in);
+    cp.ncb_out = (int32_t)wide_blocks(cp.d_out);
     if (r_max <= 32)
         launch_xside_wide<DT, 1, 2>(cp, ep, n_expand, st);
     else if (r_max <= 64)
@@ -321,7 +326,10 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const lora_quant* xq, c
         dp.gpart_bytes = (uint32_t)((int64_t)dp.walk.nslices * T_ft * 64);
         dp.err = seg_ft.err;
         dp.stop = stop;
-        hipLaunchKernelGGL(dy_pass_kernel, dim3(kStGrid), dim3(kStWaves * kWave), 0, st, dp);
+        if (xq)
+            hipLaunchKernelGGL((dy_pass_kernel<F32Operand3>), dim3(kStGrid), dim3(kStWaves * kWave), 0, st, dp);
+        else
+            hipLaunchKernelGGL((dy_pass_kernel<F32Operand<LORA_BF16>>), dim3(kStGrid), dim3(kStWaves * kWave), 0, st, dp);
         if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
         ReduceParams gr = rp;
         gr.part = dp.gpart;
@@ -404,7 +412,7 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const lora_quant* xq, c
         ep.stop = stop;
         ks = expand_plan(ep, T_ft, num_adapters, r_max, &q, &n_expand);
     }
-    if (use_wide(xq != nullptr, r_max))
+    if (use_wide(xq != nullptr, T_ft, d_in, d_out, r_max))
         return dtype == LORA_BF16 ? run_xside_wide<LORA_BF16>(cp, q, r_max, n_expand, st)
                                   : run_xside_wide<LORA_F32>(cp, q, r_max, n_expand, st);
     if (dtype == LORA_BF16 && !one_pass)

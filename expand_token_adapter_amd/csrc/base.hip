@@ -41,9 +41,9 @@ struct BasePlan {
     int32_t splits;
 };
 
-// (the same for both types of y: fp32 takes about twice as long on every tile)
-BasePlan base_plan(int64_t T, int64_t k, int64_t N) {
+BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
     const int64_t nkb = (k + kQBlock - 1) / kQBlock, groups = (nkb + 3) / 4;
+    const float rate = dtype == LORA_BF16 ? 1.f : 1.8f;  // fp32 y: four bf16 instructions a block
     BasePlan best{kTile64x64, 1};
     float least = 0.f;
     for (int kind = kTile32x64; kind < kKinds; ++kind) {
@@ -53,7 +53,7 @@ BasePlan base_plan(int64_t T, int64_t k, int64_t N) {
         for (int64_t s = std::max<int64_t>(1, std::min(groups, kCus / tiles)); s >= 1; s /= 2) {
             const int64_t rounds = (tiles * s + kCus - 1) / kCus;
             const float steps = 4.f * (float)((groups + s - 1) / s);
-            float us = (float)rounds * (c.start + std::min(steps, (float)nkb) * c.step);
+            float us = (float)rounds * (c.start + std::min(steps, (float)nkb) * c.step * rate);
             if (s > 1) us += 4.f + (float)s * (float)(T * N) * 8.f / 8e6f;
             if (least == 0.f || us < least) {
                 least = us;
@@ -109,7 +109,9 @@ int launch_base(BaseParams p, const BasePlan& b, hipStream_t st) {
 
 extern "C" size_t lora_base_product_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out) {
     if (T < 0 || d_in < 1 || d_out < 1) return 0;
-    return T == 0 ? 16 : workspace_bytes(base_plan(T, d_in, d_out), T, d_out);
+    if (T == 0) return 16;
+    return std::max(workspace_bytes(base_plan(LORA_BF16, T, d_in, d_out), T, d_out),
+                    workspace_bytes(base_plan(LORA_F32, T, d_in, d_out), T, d_out));
 }
 
 extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
@@ -123,7 +125,7 @@ extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_i
     if (rc != LORA_OK) return rc;
     // a tile's 256 rows are addressed with 32-bit byte offsets
     if (x.ld > LORA_QUANT_MAX_LD || w.ld > LORA_QUANT_MAX_LD) return LORA_ERR_UNSUPPORTED;
-    const BasePlan b = base_plan(T, d_in, d_out);
+    const BasePlan b = base_plan(dtype, T, d_in, d_out);
     if (!ws || !aligned16(ws) || ws_bytes < workspace_bytes(b, T, d_out)) return LORA_ERR_WORKSPACE;
     BaseParams p{};
     p.x = x.codes;

@@ -23,7 +23,7 @@
 // rows (32 rows x 512 bytes, gathered through perm) and its v rows are loaded
 // straight into the wave's LDS tiles, two windows in flight, and read back
 // row-wise (g) or transposed (ds_read_b64_tr_b16, dB) as MFMA operands; v
-// (fp32) enters the bf16 MFMAs as an exact hi/lo pair.
+// (fp32) enters the bf16 MFMAs as a hi/lo pair, or in full for saved 8-bit rows.
 //
 // Why rank <= 16 only: the g partials cost 2 r / C of the dY bytes each way
 // (C = slice width), and the dB accumulators (C x r fp32 per wave) bound C by
@@ -303,10 +303,11 @@ struct DyParams {
 };
 
 // Windows [w0, w1) of pair (adapter c.a, slice cs): g partials, dB tile.
+// O: the operand that fp32 v becomes.
+template <class O>
 __device__ __forceinline__ void dy_pair(const DyParams& p, const StAct& c, int cs, int w0, int w1, int slot, int vg,
                                         int64_t pair_id, const StLds& L, int wave, int lane) {
     using F = Frag<LORA_BF16>;
-    using O = F32Operand<LORA_BF16>;
     constexpr int CT = kDyCols / 16;  // 16-column tiles (16)
     constexpr int KS = kDyCols / 32;  // 32-column steps of g (8)
     const int lr = lane & 15;
@@ -534,6 +535,7 @@ __device__ __forceinline__ int st_place() {
     __shared__ __attribute__((aligned(16))) uint16_t s_b[kStBBytes / 2];              \
     const StLds L{s_t, s_s, s_r, s_b};
 
+template <class O>
 __global__ __launch_bounds__(kStWaves * kWave) __attribute__((amdgpu_waves_per_eu(1, 1)))
 void dy_pass_kernel(DyParams p) {
     LORA_ST_LDS
@@ -551,7 +553,7 @@ void dy_pass_kernel(DyParams p) {
         }
     }
     walk_pairs(p.walk, vg, gridDim.x, [&](const StAct& c, int cs, int w0, int w1, int slot, int64_t id) {
-        dy_pair(p, c, cs, w0, w1, slot, vg, id, L, wave, lane);
+        dy_pair<O>(p, c, cs, w0, w1, slot, vg, id, L, wave, lane);
     });
 }
 

@@ -229,7 +229,8 @@ __device__ __forceinline__ void contract_tile_read(Frag<DT>* qf, const char* til
     }
 }
 
-template <int DT, bool Q8>
+// OP: the operand that fp32 g / v becomes.
+template <int DT, bool Q8, class OP>
 __device__ __forceinline__ void contract_compute(const ContractWin<DT, Q8>& W, char* tile, f32x4_t (*acc)[4], int win,
                                                  int lo, int hi, int lcol, int lrow, int nmb, int lane) {
     using F = Frag<DT>;
@@ -249,7 +250,7 @@ __device__ __forceinline__ void contract_compute(const ContractWin<DT, Q8>& W, c
                 f[e] = (pp + e >= lo && pp + e < hi) ? W.pv[mb][0][e] : 0.f;
                 f[4 + e] = (pp + 4 + e >= lo && pp + 4 + e < hi) ? W.pv[mb][1][e] : 0.f;
             }
-            const F32Operand<DT> po = F32Operand<DT>::make(f);
+            const OP po = OP::make(f);
 #pragma unroll
             for (int nb = 0; nb < 4; ++nb) acc[mb][nb] = po.mma_left(qf[nb], acc[mb][nb]);
         }
@@ -266,7 +267,7 @@ __device__ __forceinline__ void contract_compute(const ContractWin<DT, Q8>& W, c
 // Body of workgroup blk of the G workgroups (NW waves each, G a multiple of
 // the 8 XCDs, workgroup blk placed at a launch index congruent to blk modulo
 // 8) that share the contraction; s_mem holds ContractLds<DT, NW>::kBytes.
-// XQ: x is saved 8-bit rows.
+// XQ: x is saved 8-bit rows; g and v then enter the bf16 instruction in full.
 template <int DT, bool NT, int NW, bool XQ>
 __device__ __forceinline__ void contract_body(const ContractParams& p, int blk, int G, char* s_mem) {
     static_assert(NW >= 4, "waves 0..3 finish the four 16-column blocks of a tile");
@@ -383,6 +384,7 @@ __device__ __forceinline__ void contract_body(const ContractParams& p, int blk, 
             auto win_at = [&](int i) { return wa + 32 * rotated(0, nw, rot, i < nw ? i : nw - 1); };
             auto windows = [&](auto q8) {
                 constexpr bool Q8 = decltype(q8)::value;
+                using OP = std::conditional_t<XQ, F32Full<DT>, F32Operand<DT>>;
                 int32_t rowsA[4], rowsB[4];
                 ContractWin<DT, Q8> WA, WB;
                 contract_rows(rowsA, p.perm, win_at(0), lo, hi, lrow);
@@ -395,14 +397,14 @@ __device__ __forceinline__ void contract_body(const ContractParams& p, int blk, 
                 // keeps B's loads where they are issued, a window ahead)
                 int i = 0;
                 for (; i + 1 < nw; i += 2) {
-                    contract_compute<DT, Q8>(WA, tileA, acc, win_at(i), lo, hi, lcol, lrow, nmb, lane);
+                    contract_compute<DT, Q8, OP>(WA, tileA, acc, win_at(i), lo, hi, lcol, lrow, nmb, lane);
                     contract_load<DT, NT, Q8>(WA, q, ldq, p.xs, p.ldxs, PT, p.ldT, rowsA, win_at(i + 2), cq, lcol, rank0, r, lane);
                     contract_rows(rowsA, p.perm, win_at(i + 4), lo, hi, lrow);
-                    contract_compute<DT, Q8>(WB, tileB, acc, win_at(i + 1), lo, hi, lcol, lrow, nmb, lane);
+                    contract_compute<DT, Q8, OP>(WB, tileB, acc, win_at(i + 1), lo, hi, lcol, lrow, nmb, lane);
                     contract_load<DT, NT, Q8>(WB, q, ldq, p.xs, p.ldxs, PT, p.ldT, rowsB, win_at(i + 3), cq, lcol, rank0, r, lane);
                     contract_rows(rowsB, p.perm, win_at(i + 5), lo, hi, lrow);
                 }
-                if (i < nw) contract_compute<DT, Q8>(WA, tileA, acc, win_at(i), lo, hi, lcol, lrow, nmb, lane);
+                if (i < nw) contract_compute<DT, Q8, OP>(WA, tileA, acc, win_at(i), lo, hi, lcol, lrow, nmb, lane);
             };
             if (XQ && is_dA)
                 windows(std::bool_constant<XQ>{});

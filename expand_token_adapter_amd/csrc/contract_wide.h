@@ -13,9 +13,6 @@
 // in LDS for the others (one barrier a window).  No sum crosses waves.  The price
 // is larger partial tiles where workgroup ranges cut a tile.
 //
-// g and v (fp32) enter the bf16 instruction as three bf16 parts, 24 bits, so
-// the products are exact and the sums are fp32 sums.
-//
 // A window of an adapter with more rank blocks takes longer: the split of the
 // work into equal ranges counts 2 + blocks for each.
 #pragma once
@@ -26,38 +23,10 @@ namespace lora {
 
 constexpr int kWideCols = 256;
 
-// An fp32 operand as hi + mid + lo bf16 parts (each the rounding of what the
-// parts before it leave: together all 24 bits).
-struct F32Operand3 {
-    Frag<LORA_BF16> part[3];
-    __device__ __forceinline__ static F32Operand3 make(const float* f) {
-        F32Operand3 o;
-        float r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = f[i];
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t h = pack_bf16x2(r[2 * i], r[2 * i + 1]);
-                o.part[k].q[i] = h;
-                r[2 * i] -= __uint_as_float(h << 16);
-                r[2 * i + 1] -= __uint_as_float(h & 0xffff0000u);
-            }
-        return o;
-    }
-    __device__ __forceinline__ f32x4_t mma_left(const Frag<LORA_BF16>& q, f32x4_t c) const {
-#pragma unroll
-        for (int k = 0; k < 3; ++k) c = mma(part[k], q, c);
-        return c;
-    }
-};
-template <int DT>
-using WideOperand = std::conditional_t<DT == LORA_BF16, F32Operand3, F32Operand<LORA_F32>>;
 template <int DT, int MB>
 struct WideLds {
     static constexpr int kTiles = ContractLds<DT, 4>::kTransBytes;
-    static constexpr int kOp = sizeof(WideOperand<DT>) / 16;  // 16-byte parts of an operand
+    static constexpr int kOp = sizeof(F32Full<DT>) / 16;  // 16-byte parts of an operand
     static constexpr int kBytes = kTiles + 2 * MB * kOp * kWave * 16;
 };
 
@@ -173,7 +142,7 @@ __device__ __forceinline__ void contract_wide_body(const ContractParams& p, int 
         abase += uniform64(__shfl(incl, kWave - 1, kWave));
     }
 
-    using OP = WideOperand<DT>;
+    using OP = F32Full<DT>;
     constexpr int kOp = WideLds<DT, MB>::kOp;
     char* tile0 = s_mem + 2 * wave * ContractLds<DT, 4>::kTileBytes;
     u32x4_t* s_op = reinterpret_cast<u32x4_t*>(s_mem + WideLds<DT, MB>::kTiles);  // [2][MB][kOp][lane]

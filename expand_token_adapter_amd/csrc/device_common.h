@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "lora_batch.h"
 
 namespace lora {
@@ -234,6 +236,40 @@ struct F32Operand<LORA_F32> {
     __device__ __forceinline__ f32x4_t mma_right(const Frag<LORA_F32>& w, f32x4_t c) const { return mma(w, f, c); }
     __device__ __forceinline__ f32x4_t mma_left(const Frag<LORA_F32>& q, f32x4_t c) const { return mma(f, q, c); }
 };
+
+// The same in full: hi + mid + lo bf16 parts, each the rounding of what the
+// parts before it leave, together all 24 bits.
+struct F32Operand3 {
+    Frag<LORA_BF16> part[3];
+    __device__ __forceinline__ static F32Operand3 make(const float* f) {
+        F32Operand3 o;
+        float r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = f[i];
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t h = pack_bf16x2(r[2 * i], r[2 * i + 1]);
+                o.part[k].q[i] = h;
+                r[2 * i] -= __uint_as_float(h << 16);
+                r[2 * i + 1] -= __uint_as_float(h & 0xffff0000u);
+            }
+        return o;
+    }
+    __device__ __forceinline__ f32x4_t mma_right(const Frag<LORA_BF16>& w, f32x4_t c) const {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) c = mma(w, part[k], c);
+        return c;
+    }
+    __device__ __forceinline__ f32x4_t mma_left(const Frag<LORA_BF16>& q, f32x4_t c) const {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) c = mma(part[k], q, c);
+        return c;
+    }
+};
+template <int DT>
+using F32Full = std::conditional_t<DT == LORA_BF16, F32Operand3, F32Operand<LORA_F32>>;
 
 // ---------------------------------------------------------------- element IO
 

@@ -153,7 +153,7 @@ def test_workspaces_of_the_caller_and_their_refusal():
     assert torch.equal(lb.lora_base_product(x, w, ws=ws[:need]), want)
     assert (ws[need:] == 255).all()
     with pytest.raises(lb.LoraError):
-        lb.lora_base_product(x, w, ws=ws[:need - 1])
+        lb.lora_base_product(x, w, ws=ws[:need // 4])
     with pytest.raises(lb.LoraError):
         lb.lora_base_product(x, w, ws=ws[8:need + 8])
 
