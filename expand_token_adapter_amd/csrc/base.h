@@ -93,26 +93,11 @@ struct QuantFrag<LORA_F32> {
     }
 };
 
-// Eight consecutive outputs of one row: added to what is there (accumulate) in
+// Four consecutive outputs of one row: added to what is there (accumulate) in
 // fp32, rounded once.
 template <int DT>
-__device__ __forceinline__ void base_store8(const BaseParams& p, int t, int n, f32x4_t v0, f32x4_t v1) {
-    if (t >= p.T || n >= p.N) return;  // (N is a multiple of 8: the eight are in or out together)
-    char* at = p.y + ((int64_t)t * p.ldy + n) * Frag<DT>::kBytes;
-    float f[8] = {v0[0], v0[1], v0[2], v0[3], v1[0], v1[1], v1[2], v1[3]};
-    if (p.accumulate) {
-        float o[8];
-        Elem<DT>::load8(at, o);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] += o[e];
-    }
-    Elem<DT>::store8(at, f);
-}
-
-// Four of them.
-template <int DT>
 __device__ __forceinline__ void base_store4(const BaseParams& p, int t, int n, f32x4_t v) {
-    if (t >= p.T || n >= p.N) return;
+    if (t >= p.T || n >= p.N) return;  // (N is a multiple of 8: the four are in or out together)
     char* at = p.y + ((int64_t)t * p.ldy + n) * Frag<DT>::kBytes;
     if constexpr (DT == LORA_BF16) {
         LORA_GLOBAL u32x2_t* d = gptr(reinterpret_cast<u32x2_t*>(at));
@@ -338,18 +323,44 @@ __global__ __launch_bounds__(WN* WT* kWave) void base_kernel(BaseParams p) {
     }
     wait_vmcnt_le<0>();  // nothing may land in LDS after the workgroup has ended
 #pragma unroll
-    for (int h = 0; h < FT; ++h)
+    for (int h = 0; h < FT; ++h) {
+        const int t = t0 + wt + 16 * h + lr;
+        const bool t_in = t < p.T;
+        if (p.splits > 1) {
+            float* row = p.part + ((int64_t)part * p.T + t) * p.N;
 #pragma unroll
-        for (int f = 0; f < FN; f += 2) {
-            const int t = t0 + wt + 16 * h + lr, n = n0 + wn + 16 * f + 8 * lg;
-            if (p.splits == 1)
-                base_store8<DT>(p, t, n, acc[f][h], acc[f + 1][h]);
-            else if (t < p.T && n < p.N) {
-                LORA_GLOBAL f32x4_t* d = gptr(reinterpret_cast<f32x4_t*>(p.part + ((int64_t)part * p.T + t) * p.N + n));
-                d[0] = acc[f][h];
-                d[1] = acc[f + 1][h];
+            for (int f = 0; f < FN; f += 2) {
+                const int n = n0 + wn + 16 * f + 8 * lg;
+                if (t_in && n < p.N) {
+                    LORA_GLOBAL f32x4_t* d = gptr(reinterpret_cast<f32x4_t*>(row + n));
+                    d[0] = acc[f][h];
+                    d[1] = acc[f + 1][h];
+                }
+            }
+            continue;
+        }
+        // Eight outputs at a time, added to what is there in fp32 and rounded once;
+        // the old values of a row are loaded together (outputs past the matrix load
+        // its first ones).
+        char* row = p.y + (t_in ? t : 0) * p.ldy * Frag<DT>::kBytes;
+        float old[FN / 2][8];
+        if (p.accumulate) {
+#pragma unroll
+            for (int f = 0; f < FN; f += 2) {
+                const int n = n0 + wn + 16 * f + 8 * lg;
+                Elem<DT>::load8(row + (int64_t)(n < p.N ? n : 0) * Frag<DT>::kBytes, old[f / 2]);
             }
         }
+#pragma unroll
+        for (int f = 0; f < FN; f += 2) {
+            const int n = n0 + wn + 16 * f + 8 * lg;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = acc[f + e / 4][h][e & 3] + (p.accumulate ? old[f / 2][e] : 0.f);
+            if (t_in && n < p.N) Elem<DT>::store8(row + (int64_t)n * Frag<DT>::kBytes, v);
+        }
+    }
 }
 
 // The sum of the parts of a split k, in order, as base_kernel stores it: a

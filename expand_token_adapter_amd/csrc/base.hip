@@ -5,10 +5,13 @@
 // k; small tiles fill the chip, large ones load less per product.  Measured
 // (us, bf16 y; rows x k x outputs):
 //                     32x64  64x64  64x128 128x128 256x128 256x256
-//    256 x  4096 x 4096  17.8    8.9    11.2    15.6    22.3    39.3
-//   1024 x  4096 x 4096  49.8   27.2    23.4    17.9    24.1    41.3
+//    256 x  4096 x 4096  13.5    9.1    11.4    15.3    23.4    40.1
+//   1024 x  4096 x 4096  49.2   27.3    23.8    18.5    24.1    41.5
 //   2048 x  4096 x 4096  98.1   51.9    45.5    34.3    29.8    42.3
-//   6783 x 4096 x 14336     -    596     522     414     348     302
+//   6783 x 4096 x 14336  1132    607     540     415     354     307
+// Small tiles are bound by the loads into LDS (64x64: 16 KB a step in 0.17 us,
+// 95 GB/s a CU), 256x256 by the matrix cores at the clock that they leave (2.6
+// PFLOP/s; the library's product with one scale for each whole operand takes 291 us).
 // Where the tiles leave CUs without work, k is split, for a second kernel that
 // adds the parts: 64 x 14336 x 4096, 64x64: 36.8 us in one part, 18.4 in four.
 // Up to 16 rows may take the weight as a stream instead: 1 x 4096 x 4096 5.8 us
@@ -94,7 +97,8 @@ int launch_base(BaseParams p, const BasePlan& b, hipStream_t st) {
         case kTile64x128: launch_tiles<DT, 64, 128, 2, 2, 4>(p, grid, st); break;
         case kTile128x128: launch_tiles<DT, 128, 128, 2, 2, 3>(p, grid, st); break;
         case kTile256x128: launch_tiles<DT, 256, 128, 2, 2, 2>(p, grid, st); break;
-        default: launch_tiles<DT, 256, 256, 2, 2, 2>(p, grid, st); break;
+        // eight waves, or for fp32 y four (6783 x 4096 x 14336: 307 against 320 us, fp32 588 against 610)
+        default: launch_tiles<DT, 256, 256, 2, DT == LORA_BF16 ? 4 : 2, 2>(p, grid, st); break;
     }
     if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
     if (p.splits > 1) {
@@ -123,8 +127,9 @@ extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_i
     if (rc == LORA_OK) rc = check_quant(w, d_in);
     if (rc == LORA_OK) rc = check_matrix(y, d_out, ldy);
     if (rc != LORA_OK) return rc;
-    // a tile's 256 rows are addressed with 32-bit byte offsets
-    if (x.ld > LORA_QUANT_MAX_LD || w.ld > LORA_QUANT_MAX_LD) return LORA_ERR_UNSUPPORTED;
+    // a tile's 256 rows are addressed with 32-bit byte offsets, rows and outputs numbered in 32 bits
+    if (x.ld > LORA_QUANT_MAX_LD || w.ld > LORA_QUANT_MAX_LD || T > INT32_MAX - 256 || d_out > INT32_MAX - 256)
+        return LORA_ERR_UNSUPPORTED;
     const BasePlan b = base_plan(dtype, T, d_in, d_out);
     if (!ws || !aligned16(ws) || ws_bytes < workspace_bytes(b, T, d_out)) return LORA_ERR_WORKSPACE;
     BaseParams p{};

@@ -88,6 +88,7 @@ def test_base_product_refusals(lib):
         assert call(x=_q(**kw)) == want and call(w=_q(**kw)) == want, kw
     huge = (1 << 22) + 128
     assert call(x=_q(ld=huge)) == UNS and call(w=_q(ld=huge)) == UNS
+    assert call(T=2 ** 31 - 1, nb=2 ** 62) == UNS and call(n=2 ** 31 - 8, ldy=2 ** 31, nb=2 ** 62) == UNS
     assert call(nb=need - 1) == WS and call(ws=None) == WS and call(ws=FAKE + 8) == WS
 
 
