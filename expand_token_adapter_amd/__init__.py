@@ -571,6 +571,8 @@ def lora_quant_rows(x: torch.Tensor, out: Optional[QuantRows] = None) -> QuantRo
     px, T, d, ldx = _rows(x, "x")
     if out is None:
         out = QuantRows.empty(T, d, dev)
+    elif not isinstance(out, QuantRows):
+        raise TypeError("out must be a QuantRows")
     elif out.T != T or out.d != d or out.device != dev:
         raise ValueError(f"out must hold {T} rows of {d} values on x's device")
     _abi.check("lora_quant_rows", _launch(dev, _abi.load().lora_quant_rows, code, px, ldx, T, d, out.c))
@@ -580,6 +582,8 @@ def lora_quant_rows(x: torch.Tensor, out: Optional[QuantRows] = None) -> QuantRo
 def lora_dequant_rows(q: QuantRows, dtype: torch.dtype = torch.bfloat16,
                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The rows that q holds, as a tensor [T, d] of dtype (or into out, whose type counts)."""
+    if not isinstance(q, QuantRows):
+        raise TypeError("q must be a QuantRows")
     if out is None:
         out = torch.empty(q.T, q.d, dtype=dtype, device=q.device)
     _on_gpu(out)
@@ -600,6 +604,8 @@ def lora_quant_weight(w: torch.Tensor, transpose: bool = False, out: Optional[Qu
     rows, cols = (d_in, d_out) if transpose else (d_out, d_in)
     if out is None:
         out = QuantWeight(*QuantWeight._buffers(rows, -(-rows // _abi.LORA_QUANT_BLOCK), cols, w.device), rows, cols)
+    elif not isinstance(out, QuantWeight):
+        raise TypeError("out must be a QuantWeight")
     elif out.d_out != rows or out.d_in != cols or out.device != w.device:
         raise ValueError(f"out must be a [{rows}, {cols}] weight on w's device")
     st = _launch(w.device, _abi.load().lora_quant_weight, code, pw, ldw, d_out, d_in, int(bool(transpose)), out.c)

@@ -248,7 +248,8 @@ int check_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, cons
 }
 
 RowsParams rows_params(int64_t ldx, int32_t T, int32_t d, const lora_quant& q) {
-    return RowsParams{nullptr, nullptr, ldx, q.codes, q.ld, q.scales, q.lds, T, d, (d + kQBlock - 1) / kQBlock};
+    return RowsParams{nullptr, nullptr, ldx, q.codes, q.ld, q.scales, q.lds, T, d,
+                      (int32_t)(((int64_t)d + kQBlock - 1) / kQBlock)};
 }
 
 }  // namespace

@@ -508,7 +508,8 @@ size_t lora_backward_quant_workspace_bytes(int dtype, int32_t T_ft, int32_t d_in
  * lora_backward from saved 8-bit rows: x holds the layer input of the
  * fine-tuning rows as lora_quant_rows saved it and is read as it is; nothing
  * is restored to memory.  dtype is the type of dy, dx, A and B.  Every other
- * argument, result and error as for lora_backward.  dX is that of
+ * argument, result and error as for lora_backward (two entries of grads do not
+ * share memory).  dX is that of
  * lora_backward on the restored rows (lora_dequant_rows) bit for bit; dA and
  * dB are too for dtype LORA_F32 where the two sum in the same order, and in
  * bf16 calls take g and v in full (lora_backward: in 16 bits).  v_saved is
