@@ -162,12 +162,12 @@ int run_dec_expand(int dtype, const float* v, int64_t ldv, int32_t v_by_pos, int
 // so the result does not depend on timing.
 constexpr int kReduceWaves = 4;
 
-// NJ: 16-rank blocks covered (16 NJ >= r_max).  Every partial is loaded
+// NJ: 16-rank blocks covered, from rank0 on.  Every partial is loaded
 // unconditionally (quads at or past r read quad 0 of the row, which exists,
 // and are dropped where they are added): conditional loads are waited for one
 // at a time, these are all in flight together.
 template <int NJ>
-__device__ __forceinline__ void shrink_reduce_body(const ReduceParams& p, f32x4_t (*s_acc)[NJ][kWave]) {
+__device__ __forceinline__ void shrink_reduce_body(const ReduceParams& p, f32x4_t (*s_acc)[NJ][kWave], int rank0) {
     if (p.stop && *p.stop) return;
     const int wave = wave_id();
     const int lane = threadIdx.x & (kWave - 1);
@@ -181,7 +181,8 @@ __device__ __forceinline__ void shrink_reduce_body(const ReduceParams& p, f32x4_
         const lora_adapter ad = load_adapter(p.adapters, rec.adapter);
         if (!adapter_ok(ad, p.r_max)) continue;  // bad entries are counted by the shrink
         const int r = ad.rank;
-        const int nj = (r + 15) / 16;
+        const int nj = (r - rank0 + 15) / 16;
+        if (nj <= 0) continue;
         const bool row_ok = n < rec.rows;
         const int pos = rec.pos0 + (row_ok ? n : 0);
         const int64_t orow = wave == 0 && p.out && !p.out_by_pos ? p.perm[pos] : pos;
@@ -191,8 +192,8 @@ __device__ __forceinline__ void shrink_reduce_body(const ReduceParams& p, f32x4_
         int qoff[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            qok[j] = 16 * j + 4 * q < r;
-            qoff[j] = qok[j] ? 16 * j + 4 * q : 0;
+            qok[j] = rank0 + 16 * j + 4 * q < r;
+            qoff[j] = qok[j] ? rank0 + 16 * j + 4 * q : 0;
         }
         f32x4_t acc[NJ];
 #pragma unroll
@@ -222,7 +223,7 @@ __device__ __forceinline__ void shrink_reduce_body(const ReduceParams& p, f32x4_
                 vv[j] = *gptr(reinterpret_cast<const f32x4_t*>(p.vsrc + vrow * p.ldvsrc + qoff[j]));
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const int k = 16 * j + 4 * q;
+                const int k = rank0 + 16 * j + 4 * q;
                 if (qok[j]) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -237,7 +238,7 @@ __device__ __forceinline__ void shrink_reduce_body(const ReduceParams& p, f32x4_
                     f32x4_t sum = acc[j];
 #pragma unroll
                     for (int w = 0; w < kReduceWaves - 1; ++w) sum += s_acc[w][j][lane];
-                    const int k = 16 * j + 4 * q;
+                    const int k = rank0 + 16 * j + 4 * q;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (k + i >= r) sum[i] = 0.f;
@@ -259,14 +260,14 @@ __device__ __forceinline__ void shrink_reduce_body(const ReduceParams& p, f32x4_
 template <int NJ>
 __global__ __launch_bounds__(kReduceWaves * kWave) void shrink_reduce_kernel(ReduceParams p) {
     __shared__ f32x4_t s_acc[kReduceWaves - 1][NJ][kWave];
-    shrink_reduce_body<NJ>(p, s_acc);
+    shrink_reduce_body<NJ>(p, s_acc, 0);
 }
 
-// The sums of two shrinks (blockIdx.y) in one launch.
-template <int NJ>
+// The sums of two shrinks (blockIdx.y) in one launch, 16 ranks a workgroup
+// (blockIdx.z; 64 ranks, 28 and 8 slices: 6.5 us, all ranks in one workgroup 8.4).
 __global__ __launch_bounds__(kReduceWaves * kWave) void shrink_reduce_pair_kernel(ReduceParams a, ReduceParams b) {
-    __shared__ f32x4_t s_acc[kReduceWaves - 1][NJ][kWave];
-    shrink_reduce_body<NJ>(blockIdx.y == 0 ? a : b, s_acc);
+    __shared__ f32x4_t s_acc[kReduceWaves - 1][1][kWave];
+    shrink_reduce_body<1>(blockIdx.y == 0 ? a : b, s_acc, 16 * (int)blockIdx.z);
 }
 
 int launch_shrink_reduce(int32_t r_max, const ReduceParams& rp, int32_t T, int32_t num_adapters, hipStream_t st);
@@ -336,15 +337,8 @@ int run_shrink_pair(int dtype, const ShrinkParams& g, const ReduceParams& gr, co
         launch_shrink_pair_t<LORA_F32>(g, v, n_g, n_v, st);
     if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
     const unsigned rgrid = (unsigned)std::min<int64_t>(SchedLayout::max_tiles16(T, num_adapters), kMaxGrid);
-    const dim3 grid(rgrid, 2), block(kReduceWaves * kWave);
-    if (g.r_max <= 16)
-        hipLaunchKernelGGL(shrink_reduce_pair_kernel<1>, grid, block, 0, st, gr, vr);
-    else if (g.r_max <= 32)
-        hipLaunchKernelGGL(shrink_reduce_pair_kernel<2>, grid, block, 0, st, gr, vr);
-    else if (g.r_max <= 64)
-        hipLaunchKernelGGL(shrink_reduce_pair_kernel<4>, grid, block, 0, st, gr, vr);
-    else
-        hipLaunchKernelGGL(shrink_reduce_pair_kernel<8>, grid, block, 0, st, gr, vr);
+    hipLaunchKernelGGL(shrink_reduce_pair_kernel, dim3(rgrid, 2, (unsigned)((g.r_max + 15) / 16)),
+                       dim3(kReduceWaves * kWave), 0, st, gr, vr);
     return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
