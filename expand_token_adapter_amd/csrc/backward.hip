@@ -53,15 +53,22 @@ int launch_shrink_reduce(int32_t r_max, const ReduceParams& rp, int32_t T, int32
 constexpr int kXsideCtrGrid = LORA_XSIDE_CTR;
 static_assert(kXsideCtrGrid % kNumXcd == 0, "whole rounds of the 8 XCDs");
 
-// Saved 8-bit rows and adapters of rank above 16 take the wide contraction where
-// its 256-column tiles give every workgroup more than 8 windows of 64 ranks:
-// below that its partial tiles cost more than the reads it saves.  us, wide
-// against contract.h's tiles, all adapters of one rank: 2048 rows, 4096 -> 14336,
-// rank 32 65 / 72, rank 64 90 / 120, rank 128 139 / 209; 4096 rows, 4096 -> 4096
-// rank 64 84 / 92; 2048 rows rank 64 62 / 57; 512 rows 52 / 35.
+// Workgroups of the wide contraction (contract_wide.h): more than one per
+// CU, as a tile's start is a chain of loads, but each cut tile costs its fix-up
+// (2048 rows of ranks 8 to 64, 4096 -> 14336, contraction and fix-up: 256 workgroups
+// 46.6 us, 320 42.6, 384 43.7, 512 49.3).
+constexpr int kWideGrid = 320;
+static_assert(kWideGrid % kNumXcd == 0, "whole rounds of the 8 XCDs");
+
+// Saved 8-bit rows and adapters of rank above 16 take it where its 256-column
+// tiles give every workgroup more than 5 windows of 64 ranks: below that its partial
+// tiles cost more than the reads it saves.  us, wide against contract.h's tiles, all
+// adapters of one rank: 2048 rows, 4096 -> 14336, rank 32 63 / 72, rank 64 87 / 120,
+// rank 128 133 / 210; 4096 -> 4096 rank 64, 4096 rows 71 / 92, 2048 rows 53 / 57,
+// 1024 rows 45 / 42, 512 rows 42 / 35.
 constexpr int64_t wide_blocks(int64_t d) { return (d + kWideCols - 1) / kWideCols; }
 constexpr bool use_wide(bool quant, int64_t T, int64_t d_in, int64_t d_out, int64_t r_max) {
-    return quant && r_max > 16 && T * (wide_blocks(d_in) + wide_blocks(d_out)) * r_max > (int64_t)8 * 32 * 64 * kXsideCtrGrid;
+    return quant && r_max > 16 && T * (wide_blocks(d_in) + wide_blocks(d_out)) * r_max > (int64_t)5 * 32 * 64 * kWideGrid;
 }
 
 // Workspace layout of lora_backward (fp32 elements): g by sorted position
@@ -87,9 +94,11 @@ struct BwdWs {
         np = std::max(np, (int64_t)dy_slices(d_out) * (T > 0 ? T : 1) * 16);
         w.part2 = round_up(w.part + np, 64);
         w.fix = round_up(w.part2 + shrink_part_floats(dtype, (int32_t)T, (int32_t)d_in, (int32_t)r_max), 64);
-        const int64_t fix = use_wide(quant, T, d_in, d_out, r_max) ? wide_fix_floats(r_max <= 32 ? 2 : 4) : kFixFloats;
-        w.fix_meta = w.fix + (int64_t)kXsideCtrGrid * 2 * fix;
-        w.dyfix = round_up(w.fix_meta + (int64_t)kXsideCtrGrid * 2 * kFixMeta, 64);
+        const bool wide = use_wide(quant, T, d_in, d_out, r_max);
+        const int64_t fix = wide ? wide_fix_floats(r_max <= 32 ? 2 : 4) : kFixFloats;
+        const int64_t slots = 2 * (wide ? kWideGrid : kXsideCtrGrid);
+        w.fix_meta = w.fix + slots * fix;
+        w.dyfix = round_up(w.fix_meta + slots * kFixMeta, 64);
         w.dymeta = w.dyfix + (int64_t)kStGrid * 2 * kDyFixFloats;
         w.total = round_up(w.dymeta + (int64_t)kStGrid * 2 * kStFixMeta, 64);
         return w;
@@ -136,10 +145,10 @@ void xside_wide_kernel(ContractParams cp, int n_ctr, ExpandParams ep, int n_expa
 
 template <int DT, int KS, int MB>
 void launch_xside_wide(const ContractParams& cp, const ExpandParams& ep, unsigned n_expand, hipStream_t st) {
-    hipLaunchKernelGGL((xside_wide_kernel<DT, KS, MB>), dim3(kXsideCtrGrid + n_expand), dim3(4 * kWave), 0, st, cp,
-                       kXsideCtrGrid, ep, (int)n_expand);
-    hipLaunchKernelGGL(contract_wide_fixup_kernel<MB>, dim3(kXsideCtrGrid, 4), dim3(4 * kWave), 0, st, cp,
-                       (int)kXsideCtrGrid);
+    hipLaunchKernelGGL((xside_wide_kernel<DT, KS, MB>), dim3(kWideGrid + n_expand), dim3(4 * kWave), 0, st, cp,
+                       kWideGrid, ep, (int)n_expand);
+    hipLaunchKernelGGL(contract_wide_fixup_kernel<MB>, dim3(kWideGrid, 4, MB), dim3(4 * kWave), 0, st, cp,
+                       (int)kWideGrid);
 }
 
 template <int DT>

@@ -60,14 +60,13 @@ __device__ __forceinline__ WideCols wide_cols(const ContractParams& p, int cb_al
 }
 
 // One 16-rank x 16-column block of dA / dB (lane: 4 ranks, 1 column): where it
-// lies and what is there, loaded when it is made.
+// lies and what is there.
 struct WideOld {
     float* dst[4];
     bool ok[4], vec;  // vec: the lane's four ranks are 16 consecutive bytes of dB
     f32x4_t old;
-    __device__ __forceinline__ WideOld() {}
-    __device__ __forceinline__ WideOld(const WideCols& w, const lora_adapter& ad, const lora_adapter_grad& gr, int rank,
-                                       int nb, int lr, int lg, int d_in) {
+    __device__ __forceinline__ void load(const WideCols& w, const lora_adapter& ad, const lora_adapter_grad& gr, int rank,
+                                         int nb, int lr, int lg, int d_in) {
         const int col = w.c0 + 16 * nb + lr;
         const int r = ad.rank;
         vec = !w.is_dA && (r & 3) == 0 && ((uintptr_t)gr.dB & 15u) == 0;
@@ -264,12 +263,19 @@ __device__ __forceinline__ void contract_wide_body(const ContractParams& p, int 
             };
             int32_t rowsA[4], rowsB[4];
             Win WA, WB;
+            // (in the loop's order: loads in another order would make the loop wait
+            // for all of them, every time, before it can use its row indices)
             contract_rows(rowsA, p.perm, win_at(0), lo, hi, lrow);
             contract_rows(rowsB, p.perm, win_at(1), lo, hi, lrow);
+            __builtin_amdgcn_sched_barrier(0);
             load(WA, rowsA, 0);
+            __builtin_amdgcn_sched_barrier(0);
             contract_rows(rowsA, p.perm, win_at(2), lo, hi, lrow);
+            __builtin_amdgcn_sched_barrier(0);
             load(WB, rowsB, 1);
+            __builtin_amdgcn_sched_barrier(0);
             contract_rows(rowsB, p.perm, win_at(3), lo, hi, lrow);
+            __builtin_amdgcn_sched_barrier(0);
             int i = 0;
             for (; i + 1 < nw; i += 2) {
                 window(WA, rowsA, 0, i);
@@ -288,12 +294,15 @@ __device__ __forceinline__ void contract_wide_body(const ContractParams& p, int 
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) {
             if (mb < nmb) {
+                if (whole) {
+                    WideOld old[4];
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) {
-                    if (whole)
-                        WideOld(wc, ad, gr, rank0 + 16 * mb, nb, lr, lg, p.d_in).add(ad.scale, acc[mb][nb]);
-                    else
-                        *gptr(f + ((wave * MB + mb) * 4 + nb) * kWave + lane) = acc[mb][nb];
+                    for (int nb = 0; nb < 4; ++nb) old[nb].load(wc, ad, gr, rank0 + 16 * mb, nb, lr, lg, p.d_in);
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) old[nb].add(ad.scale, acc[mb][nb]);
+                } else {
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) *gptr(f + ((wave * MB + mb) * 4 + nb) * kWave + lane) = acc[mb][nb];
                 }
             }
         }
@@ -312,16 +321,16 @@ __device__ __forceinline__ void contract_wide_body(const ContractParams& p, int 
 }
 
 // Adds the partial tiles of each cut tile in workgroup order, then s times the
-// sum to dA / dB.  Workgroup (g, wave tile): the tile that g owns (one at most:
-// a range that owns a cut tile ends in it), 64 of its columns; wave nb takes 16
-// of them.  Latency-bound, so what does not need each other is loaded together:
+// sum to dA / dB.  Workgroup (g, wave tile, rank block): the tile that g owns (one at most:
+// a range that owns a cut tile ends in it), 64 of its columns and 16 of its
+// ranks; wave nb takes 16 columns.  Latency-bound, so what does not need each other is loaded together:
 // the records of g and the workgroups after it, then the partial tiles, the
 // table entries and the old values (2048 rows of ranks 8 to 64, 4096 -> 14336:
 // 8.9 us in place of 13.2).
 template <int MB>
 __global__ __launch_bounds__(4 * kWave) void contract_wide_fixup_kernel(ContractParams p, int G) {
     if (p.stop && *p.stop) return;
-    const int g0 = blockIdx.x, wt = blockIdx.y;
+    const int g0 = blockIdx.x, wt = blockIdx.y, mb = blockIdx.z;
     const int nb = wave_id();
     const int lane = threadIdx.x & (kWave - 1);
     // Lane j: the record of workgroup g + j (its first slot); past the grid none.
@@ -336,24 +345,19 @@ __global__ __launch_bounds__(4 * kWave) void contract_wide_fixup_kernel(Contract
     const int32_t* m = p.fix_meta + (int64_t)g0 * 2 * kFixMeta;
     const int sl = m[0] >= 0 && m[5] ? 0 : 1;
     m += sl * kFixMeta;
-    const int nmb = m[5];
-    if (m[0] < 0 || nmb == 0) return;
+    if (m[0] < 0 || mb >= m[5]) return;
     const int32_t id0 = m[0], id1 = m[1];
     const WideCols wc = wide_cols(p, m[4], wt);
     if (wc.c0 >= wc.N) return;
-    auto part = [&](int slot, int mb) {
+    auto part = [&](int slot) {
         const f32x4_t* f = reinterpret_cast<const f32x4_t*>(p.fix + (int64_t)slot * wide_fix_floats(MB));
         return *gptr(f + ((wt * MB + mb) * 4 + nb) * kWave + lane);
     };
     const lora_adapter ad = load_adapter(p.adapters, m[2]);
     const lora_adapter_grad gr = load_grad(p.grads, m[2]);
-    f32x4_t sum[MB];
-    WideOld old[MB];
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) sum[mb] = part(g0 * 2 + sl, min(mb, nmb - 1));
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-        old[mb] = WideOld(wc, ad, gr, (m[3] * MB + min(mb, nmb - 1)) * 16, nb, lane & 15, lane >> 4, p.d_in);
+    f32x4_t sum = part(g0 * 2 + sl);
+    WideOld old;
+    old.load(wc, ad, gr, (m[3] * MB + mb) * 16, nb, lane & 15, lane >> 4, p.d_in);
     // The later workgroups holding the tile form a run after g0, those without
     // units (-2) among them; their partial tiles are loaded two at a time (past the
     // run the last one again) and added in workgroup order.
@@ -364,22 +368,16 @@ __global__ __launch_bounds__(4 * kWave) void contract_wide_fixup_kernel(Contract
         const uint64_t end_mask = __ballot(!same && m0 != -2);  // another tile, or past the grid
         const int n = end_mask ? __ffsll((long long)end_mask) - 1 : kWave;
         for (int j0 = 0; j0 < n; j0 += 2) {
-            f32x4_t pv[2][MB];
+            f32x4_t pv[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) pv[j] = part((g + min(j0 + j, n - 1)) * 2);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int mb = 0; mb < MB; ++mb) pv[j][mb] = part((g + min(j0 + j, n - 1)) * 2, min(mb, nmb - 1));
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (j0 + j < n && ((same_mask >> (j0 + j)) & 1))
-#pragma unroll
-                    for (int mb = 0; mb < MB; ++mb) sum[mb] += pv[j][mb];
+                if (j0 + j < n && ((same_mask >> (j0 + j)) & 1)) sum += pv[j];
         }
         if (n < kWave) break;
     }
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-        if (mb < nmb) old[mb].add(ad.scale, sum[mb]);
+    old.add(ad.scale, sum);
 }
 
 }  // namespace lora
