@@ -28,7 +28,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import _abi
-from ._abi import LORA_BF16, LORA_F32, LORA_MAX_RANK, LoraError
+from ._abi import LORA_BASE_PRODUCT_MAX_WORKSPACE, LORA_BF16, LORA_F32, LORA_MAX_RANK, LoraError
 
 __all__ = [
     "AdapterTable", "GradTable", "QuantRows", "QuantWeight", "Segments", "LoraError",
@@ -36,7 +36,7 @@ __all__ = [
     "lora_forward",
     "lora_forward_multi", "lora_backward", "lora_backward_preemptible", "lora_adamw_step",
     "lora_quant_rows", "lora_dequant_rows", "lora_quant_weight", "lora_base_product", "lora_backward_quant",
-    "lora_abi_version", "lora_status_string",
+    "lora_abi_version", "lora_status_string", "LORA_BASE_PRODUCT_MAX_WORKSPACE",
     "lora_segments_workspace_bytes", "lora_shrink_workspace_bytes", "lora_backward_workspace_bytes",
     "lora_segments_sched_elems", "lora_base_product_workspace_bytes", "lora_backward_quant_workspace_bytes",
 ]
@@ -614,6 +614,7 @@ def lora_quant_weight(w: torch.Tensor, transpose: bool = False, out: Optional[Qu
 
 
 def lora_base_product_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
+    """Not monotone in T; never more than LORA_BASE_PRODUCT_MAX_WORKSPACE (128 MiB)."""
     return _abi.load().lora_base_product_workspace_bytes(T, d_in, d_out)
 
 

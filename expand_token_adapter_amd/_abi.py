@@ -66,6 +66,7 @@ LORA_MAX_SLICES = 3
 
 
 LORA_QUANT_BLOCK = 128
+LORA_BASE_PRODUCT_MAX_WORKSPACE = 128 << 20
 
 
 class LoraQuant(ctypes.Structure):

@@ -74,6 +74,8 @@ BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
     return best;
 }
 
+// (a split k has no more than 2 kCus workgroups, of 256 x 256 sums at most)
+static_assert(LORA_BASE_PRODUCT_MAX_WORKSPACE >= 2 * kCus * 256 * 256 * (int)sizeof(float), "every plan fits");
 size_t workspace_bytes(const BasePlan& b, int64_t T, int64_t N) {
     return b.splits > 1 ? (size_t)b.splits * (size_t)T * (size_t)N * sizeof(float) : 16;
 }

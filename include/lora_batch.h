@@ -484,7 +484,10 @@ int lora_dequant_rows(int dtype, lora_quant q, int32_t T, int32_t d, void* x, in
 int lora_quant_weight(int dtype, const void* w, int64_t ldw, int32_t d_out, int32_t d_in, int32_t transpose,
                       lora_quant q, void* stream);
 
-/* Workspace bytes of lora_base_product (host, pure). */
+/* Workspace bytes of lora_base_product (host, pure).  More rows may need less (a
+ * long k is split where the rows leave CUs without work); no call needs more than
+ * LORA_BASE_PRODUCT_MAX_WORKSPACE. */
+#define LORA_BASE_PRODUCT_MAX_WORKSPACE (128 << 20)
 size_t lora_base_product_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out);
 
 /*

@@ -115,6 +115,33 @@ def test_pitches_of_the_backward(route):
     assert (got.wide[:, wl.d_in:] == 1).all()
 
 
+@pytest.mark.parametrize("dtype,ranks,T", [("f32", [32, 7, 20], 3100), ("bf16", [32, 7, 20], 3100), ("f32", [64, 16, 33], 1600),
+                                           ("bf16", [128, 72, 9], 1100), ("f32", [128, 72, 9], 1100)])
+def test_wide_tiles_of_every_rank_class(dtype, ranks, T):
+    """256-column tiles for r_max to 32, to 64 and to 128, v saved and not, with and without dX, against 64 bits."""
+    d_in, d_out = 4104, 4112
+    rng = np.random.default_rng(T)
+    ids = np.concatenate([np.full(T // 2, 0), rng.integers(-1, 3, size=T // 4), np.full(T - T // 2 - T // 4, 1)])
+    wl = workloads.custom(ids.astype(np.int32), ranks, d_in, d_out, dtype, seed=T, scales=[2.0, -0.5, 1.5], ft_start=0, ft_count=T,
+                          name="quant-wide")
+    c = GpuCase(wl)
+    q, dy = lb.lora_quant_rows(c.x), to_dev(wl.dy, dtype, c.dev)
+    ref = oracle.from_workload(wl)
+    xv = qh.values(q.codes.cpu().numpy(), q.scales.cpu().numpy()[:, : -(-d_in // 128)], d_in)
+    dx_ref, dA_ref, dB_ref, _, _ = oracle.backward(xv, ref["dy"], ref["ids"], ref["ranks"], ref["scales"], ref["A"], ref["B"])
+    seg = lb.lora_segments_build(c.ids, 3)
+    v = lb.lora_shrink(lb.lora_dequant_rows(q, c.x.dtype), c.table, seg)
+    for v_saved, with_dx in ((None, True), (v, False)):
+        dA, dB = ([torch.zeros(t.shape, device=c.dev) for t in m] for m in (wl.A, wl.B))
+        dx = torch.zeros(T, d_in, dtype=c.x.dtype, device=c.dev) if with_dx else None
+        lb.lora_backward_quant(q, dy, c.table, lb.GradTable(dA, dB), seg, dx=dx, v_saved=v_saved)
+        torch.cuda.synchronize()
+        errs = {f"dA{a}": rel_err(dA[a], dA_ref[a]) for a in range(3)} | {f"dB{a}": rel_err(dB[a], dB_ref[a]) for a in range(3)}
+        if with_dx:
+            errs["dx"] = rel_err(dx, dx_ref)
+        assert int(seg.err.item()) == 0 and all(e <= TOL[dtype] for e in errs.values()), errs
+
+
 def test_two_graphs_over_one_workspace():
     """A product with a split k and a wide backward, captured over the same workspace and replayed in turn."""
     c, r_max = _case("wide")

@@ -150,3 +150,13 @@ def test_the_oracle_of_the_form():
     assert c.shape == (300, 256) and s.shape == (3, 2)
     v = qh.values(c, s, 200, 128)
     assert np.all(np.abs(v - a) <= 2.0 ** -4 * np.abs(a) + 2.0 ** -10 * 2.0 ** (s.max() - 127.0))  # half a step of 4 bits
+
+
+def test_base_product_workspace_stays_below_its_bound():
+    rng = np.random.default_rng(2)
+    limit = lb.LORA_BASE_PRODUCT_MAX_WORKSPACE
+    sizes = np.exp(rng.uniform(0, np.log(1 << 20), size=(4000, 3))).astype(int) + 1
+    need = [lb.lora_base_product_workspace_bytes(int(T), 8 * int(k), 8 * int(n)) for T, k, n in sizes]
+    assert max(need) <= limit and min(need) >= 16
+    for T in range(1, 3000):  # every row count of a serving batch, one long k
+        assert lb.lora_base_product_workspace_bytes(T, 14336, 4096) <= limit
