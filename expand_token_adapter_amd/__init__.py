@@ -620,7 +620,11 @@ def lora_base_product_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
 
 def lora_base_product(x: QuantRows, w: QuantWeight, y: Optional[torch.Tensor] = None, accumulate: bool = False,
                       dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """y = W x for every row (accumulate: y += W x); without y, a new tensor [T, d_out] of dtype."""
+    """y = W x for every row (accumulate: y += W x); without y, a new tensor [T, d_out] of dtype.
+
+    Sums are fp32, rounded once.  float32 y sums exact products; for bfloat16 y the matrix instruction cuts
+    each of the 8 products of columns 8 i .. 8 i + 7 at 2^-13 of the largest (lora_batch.h states the bound):
+    a hundredth of y's rounding on ordinary rows, more only where large products of different columns cancel."""
     if not isinstance(x, QuantRows) or not isinstance(w, QuantWeight):
         raise TypeError("x must be a QuantRows and w a QuantWeight")
     if x.d != w.d_in or x.device != w.device:

@@ -1,0 +1,96 @@
+"""The 8-bit calls at the limits of what their header promises, against 64 bits.
+
+Operands are made of codes and scale bytes directly, so that they hold what
+rounded data rarely does."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import expand_token_adapter_amd as lb
+    import quant_helpers as qh
+
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}  # half a step, of the value
+
+
+def _code(v):
+    c = int(qh.encode_codes(np.array([v]))[0])
+    assert qh.E4M3[c] == v
+    return c
+
+
+def _operand(codes, byte, weight=False):
+    """QuantRows or QuantWeight of codes (numpy uint8 [n, k], k a multiple of 128) with one scale byte."""
+    n, k = codes.shape
+    scales = torch.full((-(-n // 128) if weight else n, -(-k // 512) * 4), byte, dtype=torch.uint8, device="cuda")
+    c = torch.from_numpy(codes).cuda()
+    return lb.QuantWeight(c, scales, n, k) if weight else lb.QuantRows(c, scales, k)
+
+
+def _bound(x, w, want, dt, y0=None, parts=0):
+    """Largest error of y (+)= x w^T by the header's rule, for codes with scale byte 127.
+
+    fp32 additions: the 128 products of a block one after another at the worst, then the blocks, the parts of
+    a split k and the old value, each addition off by at most 2^-23 of the magnitudes (half of that where it
+    rounds); bf16 y: the cut; at last one rounding of y."""
+    depth = 128 + x.shape[1] // 128 + parts + 1
+    mag = np.abs(x) @ np.abs(w).T + (0 if y0 is None else np.abs(y0))
+    acc = depth * 2.0 ** -23 * mag
+    if dt == torch.bfloat16:
+        X, W = (np.where(m != 0, np.maximum(np.abs(m), 2.0 ** -6), 0).reshape(m.shape[0], -1, 8) for m in (x, w))
+        top = np.stack([(X[t] * W).max(-1).sum(-1) for t in range(X.shape[0])])  # [T, N], a group at a time
+        acc = acc + 7 * 2.0 ** -13 * top
+    return acc + HALF[dt] * (np.abs(want) + acc)
+
+
+# rows of the streamed weight, and of tiles
+@pytest.mark.parametrize("T", [3, 40, 300])
+@pytest.mark.parametrize("add", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_cancelling_outliers_keep_the_bound(dtype, add, T):
+    """Groups of 8 columns in pairs: each has one product of up to 448^2 that the other cancels, beside codes of
+    every size (zeros and subnormal codes among them)."""
+    dt = TYPES[dtype]
+    rng = np.random.default_rng(T)
+    N, k = 136, 512
+    x, w = (rng.integers(0, 127, size=(m, k)).astype(np.uint8) for m in (T, N))
+    for m in (x, w):
+        m[:, rng.random(k) < 0.3] &= 15  # subnormal codes and the smallest normal ones
+        m[rng.random(m.shape) < 0.5] |= 128
+    even = np.arange(0, k, 16)
+    at = even + rng.integers(0, 8, size=even.size)
+    x[:, at] = rng.integers(100, 127, size=(T, even.size))
+    w[:, at] = rng.integers(100, 127, size=(N, even.size))
+    x[:, at + 8], w[:, at + 8] = x[:, at], w[:, at] ^ 128
+    xv, wv = qh.E4M3[x], qh.E4M3[w]
+    y0 = rng.integers(-64, 65, size=(T, N)).astype(np.float64)
+    y = torch.from_numpy(y0).to(dt).cuda() if add else None
+    got = lb.lora_base_product(_operand(x, 127), _operand(w, 127, True), y=y, accumulate=add, dtype=dt)
+    want = xv @ wv.T + (y0 if add else 0)
+    off = np.abs(got.double().cpu().numpy() - want)
+    assert (off <= _bound(xv, wv, want, dt, y0 if add else None, parts=32)).all()
+
+
+@pytest.mark.parametrize("T", [1, 64])
+@pytest.mark.parametrize("xb,wb", [(1.0, 256.0), (2.0 ** -9, 256.0), (256.0, 2.0 ** -9), (2.0 ** -9, 2.0 ** -6)])
+def test_what_is_left_of_small_products(xb, wb, T):
+    """One group holds xb * wb and 7 small products, another - xb * wb: their sum is the 7 small ones.  fp32 y has
+    them exactly; bf16 y loses no more than the header says."""
+    steps = [r for r in range(3, 17) if xb * wb * 2.0 ** -r >= 2.0 ** -18]
+    assert steps
+    for r in steps:
+        small = xb * wb * 2.0 ** -r
+        ws = max(small / max(xb * 2.0 ** -(r // 2), 2.0 ** -9), 2.0 ** -9)
+        xs = small / ws
+        x, w = np.zeros((T, 128), np.uint8), np.zeros((16, 128), np.uint8)
+        x[:, 0], x[:, 1:8], x[:, 120] = _code(xb), _code(xs), _code(xb)
+        w[:, 0], w[:, 1:8], w[:, 120] = _code(wb), _code(ws), _code(-wb)
+        xq, wq = _operand(x, 127), _operand(w, 127, True)
+        want = 7 * small
+        assert (lb.lora_base_product(xq, wq, dtype=torch.float32) == want).all(), r
+        off = (lb.lora_base_product(xq, wq).double() - want).abs().max().item()
+        X, W = max(xb, 2.0 ** -6), max(wb, 2.0 ** -6)
+        assert off <= 7 * 2.0 ** -13 * X * W * 2 + 2.0 ** -8 * want, r
