@@ -470,7 +470,9 @@ int lora_quant_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d,
 
 /*
  * Restore rows: x [T, ldx] (dtype) = the values of q, d columns (bf16: exact
- * for scale bytes from 3 to 246, else rounded to nearest even).  One kernel.
+ * for scale bytes from 3 to 246, else rounded to nearest even; magnitudes from
+ * 2^128 up, which start at byte 247 and come from saved ones of 1.9375 * 2^127 or more,
+ * are infinite in either type).  One kernel.
  */
 int lora_dequant_rows(int dtype, lora_quant q, int32_t T, int32_t d, void* x, int64_t ldx, void* stream);
 
@@ -495,7 +497,10 @@ size_t lora_base_product_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out)
  * the frozen part of h(x) = W x + B A x (MOLT, section 2.1), for every row of
  * x.  The sums (and y_t before, if added to) are fp32 and rounded once to y's
  * type; what they sum depends on that type:
- *   LORA_F32   exact products.
+ *   LORA_F32   exact products of the values as bf16 numbers, which they are for
+ *          scale bytes from 3 to 246; else they are rounded to nearest even first
+ *          (magnitudes from 2^128 up, which start at byte 247, become infinite;
+ *          LORA_BF16 takes every byte as it is).
  *   LORA_BF16  products that the matrix instruction cuts: of the 8 products of
  *          columns 8 i .. 8 i + 7 each loses what lies below 2^-13 of the power
  *          of two of the group's largest, where a code below 2^-6 (e4m3's

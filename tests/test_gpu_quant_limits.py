@@ -94,3 +94,32 @@ def test_what_is_left_of_small_products(xb, wb, T):
         off = (lb.lora_base_product(xq, wq).double() - want).abs().max().item()
         X, W = max(xb, 2.0 ** -6), max(wb, 2.0 ** -6)
         assert off <= 7 * 2.0 ** -13 * X * W * 2 + 2.0 ** -8 * want, r
+
+
+@pytest.mark.parametrize("T", [16, 127])
+@pytest.mark.parametrize("byte,wbyte", [(0, 227), (1, 227), (2, 227), (3, 227), (3, 127), (246, 27), (247, 27), (254, 20)])
+def test_products_at_the_ends_of_the_scales(byte, wbyte, T):
+    """One code a row times 2^(wbyte - 127): fp32 y takes the value as the bf16 number that a restore gives, bf16 y
+    as it is."""
+    x, w = np.zeros((T, 128), np.uint8), np.zeros((16, 128), np.uint8)
+    x[:, 5] = np.arange(T) if T == 127 else np.arange(T) * 8 + 6
+    w[:, 5] = _code(1.0)
+    xq, wq = _operand(x, byte), _operand(w, wbyte, True)
+    value = torch.from_numpy(qh.E4M3[x[:, 5]] * 2.0 ** (byte - 127))
+    times = 2.0 ** (wbyte - 127)
+    held = value.float().to(torch.bfloat16)
+    assert torch.equal(lb.lora_dequant_rows(xq)[:, 5].cpu(), held)
+    got = lb.lora_base_product(xq, wq, dtype=torch.float32).double().cpu()
+    assert torch.equal(got, (held.double() * times)[:, None].expand(T, 16))
+    assert torch.equal(lb.lora_base_product(xq, wq).double().cpu(), (value * times)[:, None].expand(T, 16))
+    assert bool(torch.isinf(held).any()) == (byte >= 247)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_largest_magnitudes_restore_as_infinity(dtype):
+    top = torch.finfo(TYPES[dtype]).max
+    x = torch.zeros(3, 128)
+    x[0, 0], x[0, 1], x[1, 0], x[2, 0] = top, -top, 1.9375 * 2.0 ** 127, 1.9296875 * 2.0 ** 127
+    back = lb.lora_dequant_rows(lb.lora_quant_rows(x.to(TYPES[dtype]).cuda()), torch.float32).cpu()
+    assert back[0, 0] == float("inf") and back[0, 1] == -float("inf")
+    assert back[1, 0] == float("inf") and back[2, 0] == 1.875 * 2.0 ** 127
