@@ -75,10 +75,14 @@ constexpr bool use_wide(bool quant, int64_t T, int64_t d_in, int64_t d_out, int6
 // (row-major and rank-major), v rank-major (two-pass path) or by sorted
 // position (streaming path, recomputed v), the split-K partials of the shrinks
 // or the streaming path's g partials (reused by the passes, which run one
-// after the other; a second set where g's and v's shrink run together), and the partial tiles of the stream-K kernels.
+// after the other), and the partial tiles of the stream-K kernels.  Where g's
+// and v's shrink run together, v's partials lie behind g's, over the rest of
+// the partials' room and the partial tiles (written only after them).  What is
+// short of that is added for the 8-bit calls; the others ask for no more than
+// the shrinks in turn need, and run them so unless the caller's buffer is longer.
 struct BwdWs {
     int64_t ldg, ldT;               // pitch of g rows; pitch of the rank-major arrays
-    int64_t g, gT, vT, vpos, part, part2, fix, fix_meta, dyfix, dymeta, total; // offsets
+    int64_t g, gT, vT, vpos, part, part2, part2_end, fix, fix_meta, dyfix, dymeta, total; // offsets
     static int32_t dy_slices(int64_t d_out) { return (int32_t)((d_out + kDyCols - 1) / kDyCols); }
     static BwdWs make(int dtype, int64_t T, int64_t d_in, int64_t d_out, int64_t r_max, bool quant) {
         BwdWs w;
@@ -92,8 +96,7 @@ struct BwdWs {
         int64_t np = std::max(shrink_part_floats(dtype, (int32_t)T, (int32_t)d_in, (int32_t)r_max),
                               shrink_part_floats(dtype, (int32_t)T, (int32_t)d_out, (int32_t)r_max));
         np = std::max(np, (int64_t)dy_slices(d_out) * (T > 0 ? T : 1) * 16);
-        w.part2 = round_up(w.part + np, 64);
-        w.fix = round_up(w.part2 + shrink_part_floats(dtype, (int32_t)T, (int32_t)d_in, (int32_t)r_max), 64);
+        w.fix = round_up(w.part + np, 64);
         const bool wide = use_wide(quant, T, d_in, d_out, r_max);
         const int64_t fix = wide ? wide_fix_floats(r_max <= 32 ? 2 : 4) : kFixFloats;
         const int64_t slots = 2 * (wide ? kWideGrid : kXsideCtrGrid);
@@ -101,6 +104,9 @@ struct BwdWs {
         w.dyfix = round_up(w.fix_meta + slots * kFixMeta, 64);
         w.dymeta = w.dyfix + (int64_t)kStGrid * 2 * kDyFixFloats;
         w.total = round_up(w.dymeta + (int64_t)kStGrid * 2 * kStFixMeta, 64);
+        w.part2 = round_up(w.part + shrink_part_floats(dtype, (int32_t)T, (int32_t)d_out, (int32_t)r_max), 64);
+        w.part2_end = round_up(w.part2 + shrink_part_floats(dtype, (int32_t)T, (int32_t)d_in, (int32_t)r_max), 64);
+        if (quant) w.total = std::max(w.total, w.part2_end);
         return w;
     }
 };
@@ -282,10 +288,11 @@ int backward_impl(int dtype, const void* x, int64_t ldx, const lora_quant* xq, c
 
     // v = A x when the caller did not save it: by sorted position for the
     // one-pass kernel, rank-major for the contraction.  Where nothing has to
-    // stand between the two, it shares its launches with g's below.
+    // stand between the two and both sets of partials have room, it shares its
+    // launches with g's below.
     ShrinkParams vp = sp;
     ReduceParams vr = rp;
-    const bool pair = !v_saved && !one_pass && !grant;
+    const bool pair = !v_saved && !one_pass && !grant && (size_t)w.part2_end * sizeof(float) <= ws_bytes;
     if (!v_saved) {
         vp.x = xq ? xq->codes : x;
         vp.ldx = xq ? xq->ld : ldx;

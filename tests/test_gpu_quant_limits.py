@@ -123,3 +123,42 @@ def test_largest_magnitudes_restore_as_infinity(dtype):
     back = lb.lora_dequant_rows(lb.lora_quant_rows(x.to(TYPES[dtype]).cuda()), torch.float32).cpu()
     assert back[0, 0] == float("inf") and back[0, 1] == -float("inf")
     assert back[1, 0] == float("inf") and back[2, 0] == 1.875 * 2.0 ** 127
+
+
+# partials of v beside g's: within the room of the partial tiles (two), of the longer set of partials too, and past
+# both (two, the last for 8-bit rows too; there lora_backward runs the shrinks in turn unless its buffer is longer)
+@pytest.mark.parametrize("dtype,T,d_in,d_out,ranks", [("bf16", 300, 520, 392, (64, 24)), ("f32", 300, 136, 2056, (33, 16)),
+                                                      ("f32", 1500, 5128, 136, (128, 9)), ("bf16", 3001, 5128, 5128, (128, 9)),
+                                                      ("bf16", 24001, 5128, 5128, (32, 5))])
+def test_backward_shrinks_together_and_in_turn(dtype, T, d_in, d_out, ranks):
+    """lora_backward in a buffer of its size, in a longer one and with a grant (which always runs the shrinks in
+    turn), and lora_backward_quant in a buffer of its size: equal bits, nothing written behind the buffer."""
+    dt = TYPES[dtype]
+    g = torch.Generator().manual_seed(T)
+    rand = lambda *s: torch.randn(*s, generator=g).to(dt).cuda()
+    q = lb.lora_quant_rows(rand(T, d_in))
+    x, dy = lb.lora_dequant_rows(q, dt), rand(T, d_out)
+    table = lb.AdapterTable([0.05 * rand(r, d_in) for r in ranks], [0.05 * rand(d_out, r) for r in ranks], [2.0, -0.5])
+    ids = torch.randint(-1, 2, (T,), generator=g).int().cuda()
+    one, status = torch.ones(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(fn, rows, extra, *more):
+        query = lb.lora_backward_quant_workspace_bytes if fn is lb.lora_backward_quant else lb.lora_backward_workspace_bytes
+        need = query(dt, T, d_in, d_out, max(ranks))
+        buf = torch.full((need + extra + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        dA, dB = [torch.ones(r, d_in, device="cuda") for r in ranks], [torch.ones(d_out, r, device="cuda") for r in ranks]
+        dx = torch.ones(T, d_in, dtype=dt, device="cuda")
+        seg = lb.lora_segments_build(ids, 2)
+        fn(rows, dy, table, lb.GradTable(dA, dB), seg, *more, dx=dx, ws=buf[:need + extra])
+        torch.cuda.synchronize()
+        assert int(seg.err.item()) == 0 and bool((buf[need + extra:] == 0xA5).all())
+        return dA + dB + [dx]
+
+    want = run(lb.lora_backward_preemptible, x, 0, one, status)
+    assert int(status.item()) == 0
+    longer = lb.lora_backward_quant_workspace_bytes(dt, T, d_in, d_out, max(ranks))
+    for got in (run(lb.lora_backward, x, 0), run(lb.lora_backward, x, longer)):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    first = run(lb.lora_backward_quant, q, 0)
+    assert torch.equal(first[-1], want[-1])  # dX
+    assert all(torch.equal(a, b) for a, b in zip(run(lb.lora_backward_quant, q, 1 << 20), first))
