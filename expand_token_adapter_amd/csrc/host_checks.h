@@ -45,6 +45,9 @@ inline unsigned grid_for(int64_t units, int per_wg, int64_t cap) {
     return (unsigned)round_up(g, 8);
 }
 
+// A launch numbers its threads along one axis in 32 bits.
+inline bool grid_fits(int64_t workgroups, int threads) { return workgroups * threads < ((int64_t)1 << 32); }
+
 inline int rank_groups(int32_t r_max) { return (r_max + 63) / 64; }
 
 // Batches with at most this many rows per adapter (T <= this * num_adapters)

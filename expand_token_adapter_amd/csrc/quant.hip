@@ -232,20 +232,21 @@ __global__ __launch_bounds__(kThreads) void quant_weight_kernel(WeightParams p) 
     }
 }
 
-unsigned rows_grid(const RowsParams& p, int units) {
+// Workgroups for T rows of d values, `units` blocks a lane.
+int64_t rows_grid(int32_t T, int32_t d, int units) {
     const int64_t per = kThreads / 16 * units;
-    return (unsigned)(((int64_t)p.T * p.nb + per - 1) / per);
+    return ((int64_t)T * ((d + (int64_t)kQBlock - 1) / kQBlock) + per - 1) / per;
 }
 
-int check_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, const lora_quant& q) {
+int check_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, const lora_quant& q, int units) {
     if (!valid_dtype(dtype) || T < 0 || d < 1) return LORA_ERR_INVALID_ARG;
     if (T == 0) return LORA_OK;
     int rc = check_matrix(x, d, ldx);
     if (rc == LORA_OK) rc = check_quant(q, d);
     if (rc != LORA_OK) return rc;
-    // blocks are numbered in 32 bits
-    return (int64_t)T * ((d + (int64_t)kQBlock - 1) / kQBlock) > INT32_MAX ? LORA_ERR_UNSUPPORTED : LORA_OK;
+    return grid_fits(rows_grid(T, d, units), kThreads) ? LORA_OK : LORA_ERR_UNSUPPORTED;
 }
+static_assert(kSaveUnits <= 8 && kRestoreUnits <= 8, "blocks are numbered in 32 bits");
 
 RowsParams rows_params(int64_t ldx, int32_t T, int32_t d, const lora_quant& q) {
     return RowsParams{nullptr, nullptr, ldx, q.codes, q.ld, q.scales, q.lds, T, d,
@@ -255,11 +256,11 @@ RowsParams rows_params(int64_t ldx, int32_t T, int32_t d, const lora_quant& q) {
 }  // namespace
 
 extern "C" int lora_quant_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, lora_quant q, void* stream) {
-    const int rc = check_rows(dtype, x, ldx, T, d, q);
+    const int rc = check_rows(dtype, x, ldx, T, d, q, kSaveUnits);
     if (rc != LORA_OK || T == 0) return rc;
     RowsParams p = rows_params(ldx, T, d, q);
     p.x = static_cast<const char*>(x);
-    const dim3 grid(rows_grid(p, kSaveUnits)), block(kThreads);
+    const dim3 grid((unsigned)rows_grid(T, d, kSaveUnits)), block(kThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (dtype == LORA_BF16)
         hipLaunchKernelGGL(quant_rows_kernel<LORA_BF16>, grid, block, 0, st, p);
@@ -269,11 +270,11 @@ extern "C" int lora_quant_rows(int dtype, const void* x, int64_t ldx, int32_t T,
 }
 
 extern "C" int lora_dequant_rows(int dtype, lora_quant q, int32_t T, int32_t d, void* x, int64_t ldx, void* stream) {
-    const int rc = check_rows(dtype, x, ldx, T, d, q);
+    const int rc = check_rows(dtype, x, ldx, T, d, q, kRestoreUnits);
     if (rc != LORA_OK || T == 0) return rc;
     RowsParams p = rows_params(ldx, T, d, q);
     p.xo = static_cast<char*>(x);
-    const dim3 grid(rows_grid(p, kRestoreUnits)), block(kThreads);
+    const dim3 grid((unsigned)rows_grid(T, d, kRestoreUnits)), block(kThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (dtype == LORA_BF16)
         hipLaunchKernelGGL(dequant_rows_kernel<LORA_BF16>, grid, block, 0, st, p);
@@ -290,9 +291,9 @@ extern "C" int lora_quant_weight(int dtype, const void* w, int64_t ldw, int32_t 
     if (rc != LORA_OK) return rc;
     if (d_out % 8 != 0) return LORA_ERR_UNSUPPORTED;
     const WeightParams p{static_cast<const char*>(w), ldw, q.codes, q.ld, q.scales, q.lds, d_out, d_in};
-    const int64_t nbs = ((int64_t)d_out + kQBlock - 1) / kQBlock;
-    if (nbs > 65535) return LORA_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)(((int64_t)d_in + kQBlock - 1) / kQBlock), (unsigned)nbs), block(kThreads);
+    const int64_t nbs = ((int64_t)d_out + kQBlock - 1) / kQBlock, kbs = ((int64_t)d_in + kQBlock - 1) / kQBlock;
+    if (nbs > 65535 || !grid_fits(kbs, kThreads)) return LORA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)kbs, (unsigned)nbs), block(kThreads);
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (dtype == LORA_BF16 && transpose)
         hipLaunchKernelGGL((quant_weight_kernel<LORA_BF16, true>), grid, block, 0, st, p);

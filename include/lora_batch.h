@@ -464,7 +464,8 @@ typedef struct lora_quant {
 /*
  * Save rows: q = the 8-bit form of x [T, ldx] (dtype), d columns.  One kernel.
  * A range of a longer matrix is saved by pointer offsets of x and q (a row of
- * q is a row of codes and a row of scales).  LORA_ERR_UNSUPPORTED for 2^31 blocks or more.
+ * q is a row of codes and a row of scales).  LORA_ERR_UNSUPPORTED for more than
+ * 2^29 - 32 blocks (a launch's threads are numbered in 32 bits): save pieces.
  */
 int lora_quant_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, lora_quant q, void* stream);
 
@@ -472,7 +473,8 @@ int lora_quant_rows(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d,
  * Restore rows: x [T, ldx] (dtype) = the values of q, d columns (bf16: exact
  * for scale bytes from 3 to 246, else rounded to nearest even; magnitudes from
  * 2^128 up, which start at byte 247 and come from saved ones of 1.9375 * 2^127 or more,
- * are infinite in either type).  One kernel.
+ * are infinite in either type).  One kernel.  LORA_ERR_UNSUPPORTED for more than
+ * 2^30 - 64 blocks.
  */
 int lora_dequant_rows(int dtype, lora_quant q, int32_t T, int32_t d, void* x, int64_t ldx, void* stream);
 
@@ -481,7 +483,8 @@ int lora_dequant_rows(int dtype, lora_quant q, int32_t T, int32_t d, void* x, in
  * 128 x 128.  transpose = 0: q is [d_out, d_in].  transpose = 1: q is the
  * transposed weight [d_in, d_out], with the transposed codes and scales of
  * the other form, for products with W^T (dX = W^T dY).  d_out and d_in
- * multiples of 8.  One kernel, once per weight.
+ * multiples of 8.  One kernel, once per weight.  LORA_ERR_UNSUPPORTED for d_out
+ * above 128 * 65535 or d_in above 2^31 - 128.
  */
 int lora_quant_weight(int dtype, const void* w, int64_t ldw, int32_t d_out, int32_t d_in, int32_t transpose,
                       lora_quant q, void* stream);

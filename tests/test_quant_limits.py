@@ -27,3 +27,26 @@ def test_backward_sizes_hold_both_sets_of_partials_for_8_bit_rows(lib):
         both = (-(-d_in // 512) + -(-d_out // 512)) * T * r * 4
         assert lib.lora_backward_quant_workspace_bytes(0, T, d_in, d_out, r) >= both
         assert lib.lora_backward_quant_workspace_bytes(0, T, d_in, d_out, r) >= lib.lora_backward_workspace_bytes(0, T, d_in, d_out, r)
+
+
+def _q(ld=128, lds=4):
+    return _abi.LoraQuant(FAKE, ld, FAKE, lds)
+
+
+@pytest.mark.parametrize("d,blocks", [(8, 1), (128, 1), (200, 2), (14336, 112)])
+def test_rows_past_a_launch_are_refused(lib, d, blocks):
+    """A launch has fewer than 2^32 threads, 8 (save) or 4 (restore) for a block of 128: more blocks are refused by
+    the call, before a launch that would fail."""
+    q = _q(ld=-(-d // 128) * 128, lds=blocks + -blocks % 4)
+    pitch = -(-d // 8) * 8
+    for limit, call in ((2 ** 29 - 32, lambda T: lib.lora_quant_rows(0, FAKE, pitch, T, d, q, None)),
+                        (2 ** 30 - 64, lambda T: lib.lora_dequant_rows(0, q, T, d, FAKE, pitch, None))):
+        T = limit // blocks + 1
+        for t in (T, T + 1, 2 * T, 2 ** 31 - 1):
+            assert call(min(t, 2 ** 31 - 1)) == _abi.LORA_ERR_UNSUPPORTED, t
+
+
+def test_weights_past_a_launch_are_refused(lib):
+    for d_out, d_in in ((8, 2 ** 31 - 8), (8, 2 ** 31 - 120), (128 * 65535 + 8, 8)):
+        for tr in (0, 1):
+            assert lib.lora_quant_weight(0, FAKE, d_in, d_out, d_in, tr, _q(ld=2 ** 31, lds=2 ** 25), None) == _abi.LORA_ERR_UNSUPPORTED
