@@ -238,11 +238,12 @@ class _Quant:
                                     ("scales", scales, scale_rows, -(-cols // (4 * block)) * 4, 4)):
             if t.dim() != 2 or t.stride(1) != 1 or t.shape[0] != r or t.shape[1] < c:
                 raise ValueError(f"{name} must be [{r}, >= {c}] with contiguous rows")
-            if r > 1 and (t.stride(0) % unit or t.stride(0) < t.shape[1]) or r == 1 and t.shape[1] % unit:
+            if r > 1 and (t.stride(0) % unit or t.stride(0) < t.shape[1]):
                 raise ValueError(f"the row pitch of {name} must be a multiple of {unit}")
         self.codes, self.scales, self.device = codes, scales, codes.device
-        self.c = _abi.LoraQuant(codes.data_ptr(), codes.stride(0) if rows > 1 else codes.shape[1],
-                                scales.data_ptr(), scales.stride(0) if scale_rows > 1 else scales.shape[1])
+        # (one row has no pitch: a slice of a wider matrix may stand at any, its own width is what counts)
+        self.c = _abi.LoraQuant(codes.data_ptr(), codes.stride(0) if rows > 1 else -(-cols // block) * block,
+                                scales.data_ptr(), scales.stride(0) if scale_rows > 1 else -(-cols // (4 * block)) * 4)
 
     @staticmethod
     def _buffers(rows: int, scale_rows: int, cols: int, device):

@@ -50,3 +50,30 @@ def test_weights_past_a_launch_are_refused(lib):
     for d_out, d_in in ((8, 2 ** 31 - 8), (8, 2 ** 31 - 120), (128 * 65535 + 8, 8)):
         for tr in (0, 1):
             assert lib.lora_quant_weight(0, FAKE, d_in, d_out, d_in, tr, _q(ld=2 ** 31, lds=2 ** 25), None) == _abi.LORA_ERR_UNSUPPORTED
+
+
+def test_any_slice_of_rows_is_rows(monkeypatch):
+    """Rows inside wider buffers: a slice of one row or none has the width and pitch that its rows need, as longer
+    slices have, and so has a weight of one row of scales."""
+    import expand_token_adapter_amd as lb
+    monkeypatch.setattr(lb, "_on_gpu", lambda *ts: None)
+    codes, scales = torch.zeros(6, 640, dtype=torch.uint8)[:, :500], torch.zeros(6, 12, dtype=torch.uint8)[:, :5]
+    q = lb.QuantRows(codes, scales, 300)
+    assert (q.c.ld, q.c.lds) == (640, 12)
+    for a, b in ((0, 6), (1, 3), (2, 3), (5, 6), (4, 4)):
+        s = q[a:b]
+        assert s.T == b - a and s.d == 300
+        if s.T > 1:
+            assert (s.c.ld, s.c.lds) == (640, 12)
+        else:
+            assert (s.c.ld, s.c.lds) == (384, 4)
+        if s.T:
+            assert (s.c.codes, s.c.scales) == (codes[a:].data_ptr(), scales[a:].data_ptr())
+    w = lb.QuantWeight(codes, scales[:1], 6, 300)
+    assert (w.c.ld, w.c.lds) == (640, 4)
+    with pytest.raises(ValueError):
+        lb.QuantRows(codes[:, :380], scales, 300)  # too narrow for three blocks
+    with pytest.raises(ValueError):
+        lb.QuantRows(torch.zeros(6, 500, dtype=torch.uint8), scales, 300)  # pitch 500
+    with pytest.raises(ValueError):
+        lb.QuantRows(codes[:1, :380], scales[:1], 300)
