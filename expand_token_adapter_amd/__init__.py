@@ -500,13 +500,14 @@ def lora_backward_quant(x: QuantRows, dy: torch.Tensor, adapters: AdapterTable, 
 
     The gradients (+=) are those of lora_backward on lora_dequant_rows(x): dX bit for bit, dA and dB
     with g and v in full."""
-    if not isinstance(x, QuantRows):
-        raise TypeError("x must be a QuantRows (lora_quant_rows)")
     _backward("lora_backward_quant", x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, ())
 
 
 def _backward(fn, x, dy, adapters, grads, seg_ft, dx, v_saved, r_max, ws, extra) -> None:
-    quant = isinstance(x, QuantRows)
+    quant = fn == "lora_backward_quant"
+    if isinstance(x, QuantRows) != quant:
+        raise TypeError("x must be a QuantRows (lora_quant_rows)" if quant else
+                        f"{fn}: x must be a tensor (lora_backward_quant takes 8-bit rows)")
     if quant:
         T, d_in, rows = x.T, x.d, (x.c,)
         if x.device != adapters.device:

@@ -77,3 +77,24 @@ def test_any_slice_of_rows_is_rows(monkeypatch):
         lb.QuantRows(torch.zeros(6, 500, dtype=torch.uint8), scales, 300)  # pitch 500
     with pytest.raises(ValueError):
         lb.QuantRows(codes[:1, :380], scales[:1], 300)
+
+
+def test_backward_names_rows_of_the_wrong_form(monkeypatch):
+    """8-bit rows given to the calls that take tensors, and a tensor to the one that takes 8-bit rows."""
+    import expand_token_adapter_amd as lb
+    monkeypatch.setattr(lb, "_on_gpu", lambda *ts: None)
+    q = lb.QuantRows(torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8), 8)
+    dy, status = torch.zeros(4, 8), torch.zeros(1, dtype=torch.int32)
+
+    class Table:  # of adapters 8 -> 8, as far as the checks before x's read it
+        device, d_in, d_out, dtype, r_max = torch.device("cpu"), 8, 8, torch.bfloat16, 8
+
+        def __len__(self):
+            return 1
+
+    with pytest.raises(TypeError, match="lora_backward_quant"):
+        lb.lora_backward(q, dy, Table(), None, None)
+    with pytest.raises(TypeError, match="lora_backward_quant"):
+        lb._backward("lora_backward_preemptible", q, dy, Table(), None, None, None, None, None, None, (0, status.data_ptr()))
+    with pytest.raises(TypeError, match="QuantRows"):
+        lb.lora_backward_quant(torch.zeros(4, 8), dy, Table(), None, None)
