@@ -32,6 +32,7 @@
 
 #include <type_traits>
 
+#include "base_plan.h"
 #include "quant.h"
 
 namespace lora {
@@ -129,19 +130,7 @@ __device__ __forceinline__ void base_store4(const BaseParams& p, int64_t t, int 
 // The scales of up to BaseLds::kGroups * 4 blocks lie in LDS too, four blocks'
 // bytes of one row in a word; a longer k is taken in pieces.
 
-constexpr int kLdsBytes = 160 * 1024;  // of a CU
 constexpr int kBand = 4;
-
-template <int BN, int BT, int ST>
-struct BaseLds {
-    static constexpr int kStage = (BN + BT) * kQBlock;
-    static constexpr int kNB = BN > kQBlock ? BN / kQBlock : 1;  // 128-row blocks of the weight tile
-    static constexpr int kWeight = kNB * kWave * 4;              // bytes of the weight's scale words
-    static constexpr int kFit = (kLdsBytes - ST * kStage - kWeight) / (BT * 4);
-    static constexpr int kGroups = kFit < 32 ? kFit : 32;
-    static constexpr int kBytes = ST * kStage + kWeight + kGroups * BT * 4;
-    static_assert(kGroups >= 8, "room for the scales of 4096 columns");
-};
 
 template <int BN, int BT, int WN, int WT, int ST, int DT>
 __global__ __launch_bounds__(WN* WT* kWave) void base_kernel(BaseParams p) {

@@ -6,6 +6,8 @@ import numpy as np
 import pytest
 import torch
 
+import quant_plans
+
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
@@ -162,3 +164,49 @@ def test_backward_shrinks_together_and_in_turn(dtype, T, d_in, d_out, ranks):
     first = run(lb.lora_backward_quant, q, 0)
     assert torch.equal(first[-1], want[-1])  # dX
     assert all(torch.equal(a, b) for a, b in zip(run(lb.lora_backward_quant, q, 1 << 20), first))
+
+
+# ---------------------------------------------------------------- products through every kernel
+
+def _values(codes, scales, k, rows=1):
+    """Values (float64, on the GPU) of codes, and 2^-6 times their blocks' scales."""
+    table = torch.from_numpy(qh.E4M3).cuda()
+    v = table.index_select(0, codes[:, :k].reshape(-1).int()).view(codes.shape[0], k)
+    s = torch.ldexp(torch.ones((), dtype=torch.float64, device="cuda"), scales.int() - 127)
+    s = s.repeat_interleave(rows, 0)[: codes.shape[0]].repeat_interleave(128, 1)[:, :k]
+    return v * s, s * 2.0 ** -6
+
+
+def _cut_terms(v, floor):
+    """Largest counted magnitude of each group of 8 columns."""
+    return torch.where(v != 0, torch.maximum(v.abs(), floor), 0.0).view(v.shape[0], -1, 8).amax(-1)
+
+
+@pytest.mark.parametrize("dtype,T,k,n,kernel,parts,pieces", quant_plans.PRODUCTS)
+def test_product_of_every_kernel(dtype, T, k, n, kernel, parts, pieces):
+    """Stored and added, against 64 bits (on the GPU), with ragged edges; nothing beside y changes, and the bits are
+    the same a second time."""
+    dt = TYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(T + k + n)
+    x = torch.randn(T, k, device="cuda", generator=g) * torch.exp(2 * torch.randn(T, 1, device="cuda", generator=g))
+    x[:, ::37] *= 30
+    xq = lb.lora_quant_rows(x)
+    wq = lb.lora_quant_weight(0.02 * torch.randn(n, k, device="cuda", generator=g))
+    (xv, xf), (wv, wf) = _values(xq.codes, xq.scales, k), _values(wq.codes, wq.scales, k, 128)
+    product, mag = xv @ wv.T, xv.abs() @ wv.abs().T
+    cut = 7 * 2.0 ** -13 * (_cut_terms(xv, xf) @ _cut_terms(wv, wf).T) if dtype == "bf16" else 0.0
+    y0 = torch.randn(T, n, device="cuda", generator=g).to(dt)
+    for add in (False, True):
+        y = torch.full((T + 2, n + 8), 3.0, dtype=dt, device="cuda")
+        y[1:T + 1, :n] = y0
+        lb.lora_base_product(xq, wq, y=y[1:T + 1, :n], accumulate=add)
+        want = product + (y0.double() if add else 0.0)
+        depth = 128 + -(-k // 128) + parts + 1  # as in _bound
+        acc = depth * 2.0 ** -23 * (mag + (y0.double().abs() if add else 0.0)) + cut
+        bound = acc + HALF[dt] * (want.abs() + acc)
+        off = (y[1:T + 1, :n].double() - want).abs()
+        assert bool((off <= bound).all()), (add, float((off / bound).max()))
+        assert bool((y[0] == 3).all() and (y[T + 1] == 3).all() and (y[:, n:] == 3).all())
+        again = y0.clone()
+        lb.lora_base_product(xq, wq, y=again, accumulate=add)
+        assert torch.equal(again, y[1:T + 1, :n])

@@ -1,9 +1,15 @@
 """Limits of the 8-bit calls and of the calls beside them that hold without a GPU:
 workspace sizes, refusals, and which kernels the tests' shapes reach."""
+import math
+import os
+import random
+import subprocess
+
 import pytest
 import torch
 
 from expand_token_adapter_amd import _abi
+from quant_plans import PRODUCTS
 
 FAKE = 0x10000  # an aligned address that no check reads
 
@@ -98,3 +104,61 @@ def test_backward_names_rows_of_the_wrong_form(monkeypatch):
         lb._backward("lora_backward_preemptible", q, dy, Table(), None, None, None, None, None, None, (0, status.data_ptr()))
     with pytest.raises(TypeError, match="QuantRows"):
         lb.lora_backward_quant(torch.zeros(4, 8), dy, Table(), None, None)
+
+
+# ---------------------------------------------------------------- which kernel a product takes
+
+PLAN = """
+#include <stdio.h>
+#include "base_plan.h"
+using namespace lora;
+template <int K>
+int piece() { return 4 * BaseLds<kTiles[K].bn, kTiles[K].bt, kTiles[K].stages>::kGroups; }
+int main() {
+    const int pieces[kKinds] = {INT32_MAX, piece<1>(), piece<2>(), piece<3>(), piece<4>(), piece<5>(), piece<6>()};
+    long dt, T, k, n;
+    while (scanf("%ld %ld %ld %ld", &dt, &T, &k, &n) == 4) {
+        const BasePlan b = base_plan((int)dt, T, k, n);
+        const long nkb = (k + 127) / 128, groups = (nkb + 3) / 4, part = (groups + b.splits - 1) / b.splits * 4;
+        const long most = part < nkb ? part : nkb;
+        const BaseTile& c = kTiles[b.kind];
+        printf("%dx%d %d %ld %zu\\n", c.bn, c.bt, b.splits, (most + pieces[b.kind] - 1) / pieces[b.kind],
+               base_workspace_bytes(b, T, n));
+    }
+    return 0;
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    """(type, rows, k, outputs) of each product -> (tile, parts of k, pieces of a part, workspace bytes)."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    d = tmp_path_factory.mktemp("plan")
+    (d / "plan.cpp").write_text(PLAN)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", os.path.join(root, "include"), "-I",
+                    os.path.join(root, "expand_token_adapter_amd", "csrc"), str(d / "plan.cpp"), "-o", str(d / "plan")], check=True)
+
+    def ask(sizes):
+        text = "".join(f"{int(dt == 'f32')} {T} {k} {n}\n" for dt, T, k, n in sizes)
+        out = subprocess.run([str(d / "plan")], input=text, check=True, capture_output=True, text=True).stdout.split("\n")
+        return [(t.replace("0x0", "stream"), int(s), int(p), int(w)) for t, s, p, w in (l.split() for l in out if l)]
+
+    return ask
+
+
+def test_listed_products_take_the_kernels_they_are_listed_for(plan):
+    got = plan([s[:4] for s in PRODUCTS])
+    assert [(*s[:4], *g[:3]) for s, g in zip(PRODUCTS, got)] == PRODUCTS
+
+
+def test_listed_products_take_every_kernel(plan, lib):
+    """Nothing that the choice reaches is left out of the list: 40 000 sizes over the whole range."""
+    listed = {(s[0], s[4], s[5] > 1, s[6] > 1) for s in PRODUCTS}
+    rng = random.Random(1)
+    log = lambda lo, hi: int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))
+    sizes = [(rng.choice(["bf16", "f32"]), log(1, 10000), 8 * log(1, 16000), 8 * log(1, 8000)) for _ in range(40000)]
+    got = plan(sizes)
+    assert {(s[0], g[0], g[1] > 1, g[2] > 1) for s, g in zip(sizes, got)} <= listed
+    for s, g in zip(sizes[:500], got):
+        assert g[3] <= lib.lora_base_product_workspace_bytes(*s[1:])
