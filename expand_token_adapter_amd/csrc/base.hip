@@ -13,6 +13,7 @@ namespace {
 template <int DT, int KIND, int WN, int WT>
 void launch_tiles(const BaseParams& p, unsigned grid, hipStream_t st) {
     constexpr BaseTile c = kTiles[KIND];
+    static_assert(WN * WT * kWave <= c.threads, "the plan's bound on the launch");
     hipLaunchKernelGGL((base_kernel<c.bn, c.bt, WN, WT, c.stages, DT>), dim3(grid), dim3(WN * WT * kWave), 0, st, p);
 }
 
@@ -27,9 +28,7 @@ int launch_base(BaseParams p, const BasePlan& b, hipStream_t st) {
     const BaseTile& c = kTiles[b.kind];
     p.tiles_n = (p.N + c.bn - 1) / c.bn;
     p.tiles_t = (p.T + c.bt - 1) / c.bt;
-    const int64_t tasks = (int64_t)p.tiles_n * p.tiles_t * p.splits;
-    if (tasks > INT32_MAX - kNumXcd * kBand) return LORA_ERR_UNSUPPORTED;
-    const unsigned grid = (unsigned)round_up(tasks, kNumXcd);
+    const unsigned grid = (unsigned)round_up((int64_t)p.tiles_n * p.tiles_t * p.splits, kNumXcd);
     switch (b.kind) {
         case kTile32x64: launch_tiles<DT, kTile32x64, 1, 4>(p, grid, st); break;
         case kTile64x64: launch_tiles<DT, kTile64x64, 2, 2>(p, grid, st); break;
@@ -70,6 +69,7 @@ extern "C" int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_i
     if (x.ld > LORA_QUANT_MAX_LD || w.ld > LORA_QUANT_MAX_LD || T > INT32_MAX - 256 || d_out > INT32_MAX - 256)
         return LORA_ERR_UNSUPPORTED;
     const BasePlan b = base_plan(dtype, T, d_in, d_out);
+    if (b.kind == kKinds) return LORA_ERR_UNSUPPORTED;
     if (!ws || !aligned16(ws) || ws_bytes < base_workspace_bytes(b, T, d_out)) return LORA_ERR_WORKSPACE;
     BaseParams p{};
     p.x = x.codes;

@@ -27,7 +27,7 @@
 
 #include <algorithm>
 
-#include "lora_batch.h"
+#include "host_checks.h"
 
 namespace lora {
 
@@ -48,12 +48,13 @@ constexpr int kCus = 256;
 enum { kStream = 0, kTile32x64, kTile64x64, kTile64x128, kTile128x128, kTile256x128, kTile256x256, kKinds };
 struct BaseTile {
     int32_t bn, bt, stages;       // outputs, rows, stages of the ring in LDS
+    int32_t threads;              // of a workgroup, at most
     float start, step, step_f32;  // us of a workgroup: its start and end, a step along k (bf16, fp32 y)
 };
-constexpr BaseTile kTiles[kKinds] = {{0, 0, 0, 0.f, 0.f, 0.f},           {32, 64, 6, 0.5f, 0.151f, 0.289f},
-                                     {64, 64, 4, 0.85f, 0.198f, 0.306f},  {64, 128, 4, 1.2f, 0.351f, 0.58f},
-                                     {128, 128, 3, 2.4f, 0.45f, 0.81f},  {256, 128, 2, 3.5f, 0.677f, 1.518f},
-                                     {256, 256, 2, 3.1f, 1.122f, 2.93f}};
+constexpr BaseTile kTiles[kKinds] = {{0, 0, 0, 0, 0.f, 0.f, 0.f},             {32, 64, 6, 256, 0.5f, 0.151f, 0.289f},
+                                     {64, 64, 4, 256, 0.85f, 0.198f, 0.306f},  {64, 128, 4, 256, 1.2f, 0.351f, 0.58f},
+                                     {128, 128, 3, 256, 2.4f, 0.45f, 0.81f},  {256, 128, 2, 256, 3.5f, 0.677f, 1.518f},
+                                     {256, 256, 2, 512, 3.1f, 1.122f, 2.93f}};
 constexpr int32_t kSplits[] = {1, 2, 3, 4, 6, 8, 13, 16, 25, 32};
 constexpr int kStreamRows = 16;
 constexpr int kStreamWaves = 8;
@@ -63,10 +64,11 @@ struct BasePlan {
     int32_t splits;
 };
 
+// kind: kKinds if no kernel's launch holds the call.
 inline BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
     const int32_t nkb = (int32_t)((k + LORA_QUANT_BLOCK - 1) / LORA_QUANT_BLOCK), groups = (nkb + 3) / 4;
     const float outputs = (float)T * (float)N;
-    BasePlan best{kTile64x64, 1};
+    BasePlan best{kKinds, 1};
     float least = 0.f;
     for (int kind = kTile32x64; kind < kKinds; ++kind) {
         const BaseTile& c = kTiles[kind];
@@ -74,6 +76,7 @@ inline BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
         const int64_t tiles = (int64_t)(((uint32_t)N + c.bn - 1) / c.bn) * (((uint32_t)T + c.bt - 1) / c.bt);
         for (const int32_t s : kSplits) {
             if (s > 1 && (s > groups || tiles * s > 2 * kCus)) break;
+            if (!grid_fits(tiles * s + 8, c.threads)) break;  // (rounded up to the XCDs)
             const float rounds = (float)((uint64_t)(tiles * s + kCus - 1) / kCus);
             float us = rounds * (c.start + (float)std::min(4 * ((groups + s - 1) / s), nkb) * step);
             if (s > 1) us += 2.5f + (float)s * (0.14f + outputs * 0.97e-6f);
@@ -83,7 +86,8 @@ inline BasePlan base_plan(int dtype, int64_t T, int64_t k, int64_t N) {
             }
         }
     }
-    if (T <= kStreamRows && (float)nkb * (0.14f + 0.0017f * (float)(T - 1)) + (float)N * (float)k / 29e6f - 0.7f < least)
+    if (T <= kStreamRows && grid_fits((N + 15) / 16, kStreamWaves * 64) &&
+        (float)nkb * (0.14f + 0.0017f * (float)(T - 1)) + (float)N * (float)k / 29e6f - 0.7f < least)
         best = BasePlan{kStream, 1};
     return best;
 }

@@ -520,6 +520,8 @@ size_t lora_base_product_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out)
  *   ws: lora_base_product_workspace_bytes(T, d_in, d_out) bytes.
  * Rows are independent: a NaN in one does not reach another.  The order of
  * every sum is fixed by the shapes: results are bit-reproducible.
+ * LORA_ERR_UNSUPPORTED for pitches of codes above LORA_QUANT_MAX_LD, T or d_out
+ * above 2^31 - 257, and more outputs than one launch's tiles (2^39) hold.
  */
 int lora_base_product(int dtype, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
                       int64_t ldy, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);

@@ -119,6 +119,10 @@ int main() {
     long dt, T, k, n;
     while (scanf("%ld %ld %ld %ld", &dt, &T, &k, &n) == 4) {
         const BasePlan b = base_plan((int)dt, T, k, n);
+        if (b.kind == kKinds) {
+            printf("none 1 1 %zu\\n", base_workspace_bytes(b, T, n));
+            continue;
+        }
         const long nkb = (k + 127) / 128, groups = (nkb + 3) / 4, part = (groups + b.splits - 1) / b.splits * 4;
         const long most = part < nkb ? part : nkb;
         const BaseTile& c = kTiles[b.kind];
@@ -162,3 +166,24 @@ def test_listed_products_take_every_kernel(plan, lib):
     assert {(s[0], g[0], g[1] > 1, g[2] > 1) for s, g in zip(sizes, got)} <= listed
     for s, g in zip(sizes[:500], got):
         assert g[3] <= lib.lora_base_product_workspace_bytes(*s[1:])
+
+
+def _threads(tile, parts, T, n):
+    bn, bt = (16, 1 << 31) if tile == "stream" else map(int, tile.split("x"))
+    return (-(-n // bn) * -(-T // bt) * parts + 7) * (512 if tile in ("stream", "256x256") else 256)
+
+
+def test_products_of_very_many_rows_or_outputs_fit_a_launch(plan, lib):
+    """The choice passes over kernels whose launch would have 2^32 threads or more; what none holds is refused before
+    a launch that would fail."""
+    rows, outputs = [2 ** 20, 2 ** 26, 2 ** 30, 2 ** 30 + 64, 2 ** 31 - 264], [8, 128, 2 ** 20, 2 ** 27, 2 ** 27 + 8, 2 ** 31 - 264]
+    sizes = [(dt, T, k, n) for dt in ("bf16", "f32") for k in (8, 128, 4096) for T in [1, 3, 16, 17, 300] + rows
+             for n in outputs] + [(dt, T, k, n) for dt in ("bf16", "f32") for k in (8, 128, 4096) for T in rows for n in outputs[:3]]
+    for (dt, T, k, n), (tile, parts, _, need) in zip(sizes, plan(sizes)):
+        if tile != "none":
+            assert _threads(tile, parts, T, n) < 2 ** 32, (dt, T, k, n, tile)
+        else:
+            assert (T + n) * -(-k // 128) * 128 + T * n * (4 if dt == "f32" else 2) > 288e9  # more than a GPU holds
+            q = _q(ld=4096, lds=32)
+            assert lib.lora_base_product(int(dt == "f32"), q, T, k, q, n, FAKE, n, 0, FAKE, 2 ** 62, None) == _abi.LORA_ERR_UNSUPPORTED
+            assert need == 16
