@@ -383,7 +383,7 @@ __global__ __launch_bounds__(kSumThreads) void base_sum_kernel(BaseParams p) {
 
 // ------------------------------------------------------------------ few rows: the weight as a stream
 //
-// Up to 16 FT rows: the weight is read once, straight into operand registers,
+// Up to kStreamRows = 16 rows: the weight is read once, straight into operand registers,
 // and nothing of it is shared between waves.  A workgroup of NW waves computes
 // 16 outputs of every row; wave w takes the blocks w, w + NW, ... along k (a
 // workgroup reads NW * 128 consecutive bytes of each of its 16 weight rows at a
@@ -392,28 +392,22 @@ __global__ __launch_bounds__(kSumThreads) void base_sum_kernel(BaseParams p) {
 // 1 x 12232 x 352 11.0 us as without, 1 x 4096 x 14336 17.1 against 14.7).
 constexpr int kU = 4;
 
-template <int FT, int NW, int DT>
+template <int NW, int DT>
 __global__ __launch_bounds__(NW* kWave) void base_stream_kernel(BaseParams p) {
-    __shared__ f32x4_t s_acc[NW][FT][kWave];
+    __shared__ f32x4_t s_acc[NW][kWave];
     const int wave = wave_id();
     const int lane = threadIdx.x & (kWave - 1);
     const int lr = lane & 15, lg = lane >> 4;
     const int n0 = blockIdx.x * 16;
     const LORA_GLOBAL uint8_t* w = gptr(p.w + (int64_t)min(n0 + lr, p.N - 1) * p.ldw + 16 * lg);
     const uint8_t* ws = p.ws + (int64_t)(n0 / kQBlock) * p.ldws;
-    const LORA_GLOBAL uint8_t *x[FT], *xs[FT];
-#pragma unroll
-    for (int f = 0; f < FT; ++f) {
-        const int64_t t = min(16 * f + lr, p.T - 1);
-        x[f] = gptr(p.x + t * p.ldx + 16 * lg);
-        xs[f] = gptr(p.xs + t * p.ldxs);
-    }
-    f32x4_t acc[FT];
-#pragma unroll
-    for (int f = 0; f < FT; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const int64_t row = min(lr, p.T - 1);
+    const LORA_GLOBAL uint8_t* x = gptr(p.x + row * p.ldx + 16 * lg);
+    const LORA_GLOBAL uint8_t* xs = gptr(p.xs + row * p.ldxs);
+    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
     for (int k0 = wave; k0 < p.nkb; k0 += NW * kU) {
-        QuantOperand a[kU], b[kU][FT];
-        uint32_t as[kU], bs[kU][FT];
+        QuantOperand a[kU], b[kU];
+        uint32_t as[kU], bs[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int kb = min(k0 + NW * u, p.nkb - 1);
@@ -423,31 +417,24 @@ __global__ __launch_bounds__(NW* kWave) void base_stream_kernel(BaseParams p) {
                 a[u].u[i] = __builtin_nontemporal_load(reinterpret_cast<const LORA_GLOBAL u32x4_t*>(w + off + 64 * i));
             as[u] = cptr(ws)[kb];
 #pragma unroll
-            for (int f = 0; f < FT; ++f) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    b[u][f].u[i] = *reinterpret_cast<const LORA_GLOBAL u32x4_t*>(x[f] + off + 64 * i);
-                bs[u][f] = xs[f][kb];
-            }
+            for (int i = 0; i < 2; ++i) b[u].u[i] = *reinterpret_cast<const LORA_GLOBAL u32x4_t*>(x + off + 64 * i);
+            bs[u] = xs[kb];
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             if (k0 + NW * u < p.nkb) {
                 const QuantFrag<DT> af = QuantFrag<DT>::template make<0>(a[u], as[u]);
-#pragma unroll
-                for (int f = 0; f < FT; ++f)
-                    acc[f] = af.template mma<0>(QuantFrag<DT>::template make<0>(b[u][f], bs[u][f]), acc[f]);
+                acc = af.template mma<0>(QuantFrag<DT>::template make<0>(b[u], bs[u]), acc);
             }
         }
     }
-#pragma unroll
-    for (int f = 0; f < FT; ++f) s_acc[wave][f][lane] = acc[f];
+    s_acc[wave][lane] = acc;
     __syncthreads();
-    if (wave < FT) {
-        f32x4_t sum = s_acc[0][wave][lane];
+    if (wave == 0) {
+        f32x4_t sum = s_acc[0][lane];
 #pragma unroll
-        for (int v = 1; v < NW; ++v) sum += s_acc[v][wave][lane];
-        const int t = 16 * wave + lr, n = n0 + 4 * lg;
+        for (int v = 1; v < NW; ++v) sum += s_acc[v][lane];
+        const int t = lr, n = n0 + 4 * lg;
         if (t < p.T && n < p.N)  // (N is a multiple of 8: the four are in or out together)
             base_store4<DT>(p, t, n, sum, p.accumulate ? base_load4<DT>(p, t, n) : f32x4_t{0.f, 0.f, 0.f, 0.f});
     }

@@ -21,7 +21,7 @@ template <int DT>
 int launch_base(BaseParams p, const BasePlan& b, hipStream_t st) {
     p.splits = b.splits;
     if (b.kind == kStream) {
-        hipLaunchKernelGGL((base_stream_kernel<kStreamRows / 16, kStreamWaves, DT>), dim3((unsigned)((p.N + 15) / 16)),
+        hipLaunchKernelGGL((base_stream_kernel<kStreamWaves, DT>), dim3((unsigned)((p.N + 15) / 16)),
                            dim3(kStreamWaves * kWave), 0, st, p);
         return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
     }

@@ -56,7 +56,7 @@ constexpr BaseTile kTiles[kKinds] = {{0, 0, 0, 0, 0.f, 0.f, 0.f},             {3
                                      {128, 128, 3, 256, 2.4f, 0.45f, 0.81f},  {256, 128, 2, 256, 3.5f, 0.677f, 1.518f},
                                      {256, 256, 2, 512, 3.1f, 1.122f, 2.93f}};
 constexpr int32_t kSplits[] = {1, 2, 3, 4, 6, 8, 13, 16, 25, 32};
-constexpr int kStreamRows = 16;
+constexpr int kStreamRows = 16;  // one operand's rows
 constexpr int kStreamWaves = 8;
 
 struct BasePlan {
