@@ -55,8 +55,8 @@ static_assert(kXsideCtrGrid % kNumXcd == 0, "whole rounds of the 8 XCDs");
 
 // Workgroups of the wide contraction (contract_wide.h): more than one per
 // CU, as a tile's start is a chain of loads, but each cut tile costs its fix-up
-// (2048 rows of ranks 8 to 64, 4096 -> 14336, contraction and fix-up: 256 workgroups
-// 46.6 us, 320 42.6, 384 43.7, 512 49.3).
+// (the one shape swept, 2048 rows of ranks 8 to 64, 4096 -> 14336, contraction and
+// fix-up: 256 workgroups 46.6 us, 320 42.6, 384 43.7, 512 49.3).
 constexpr int kWideGrid = 320;
 static_assert(kWideGrid % kNumXcd == 0, "whole rounds of the 8 XCDs");
 

@@ -97,9 +97,10 @@ struct RowsParams {
 // 16 lanes take one block of 128, 8 values (16 bytes of bf16, 8 codes) a lane:
 // a wave's load is 1 KB of bf16 and its store 512 bytes of codes.  Each takes a
 // few blocks, all loads in flight at once.  Streams: 4096 x 5120 bf16 rows are
-// saved in 10.5 us (6.0 TB/s, 13.9 us from HBM; with 1 and 4 blocks 11.3 and
-// 11.0) and restored in 9.9 (with 1 and 2 blocks 11.1 and 10.2); a large copy runs
-// at 5.1 TB/s.  What bounds the save beside memory is vector work: the magnitudes
+// saved in 10.5 us (with 1 and 4 blocks 11.3 and 11.0) and restored in 9.9 (with 1
+// and 2 blocks 11.1 and 10.2) with part of the data in the last-level cache, in
+// 14.5 and 14.2 us (4.4 TB/s) from HBM, fp32 rows in 21.0 and 27.1; a large copy
+// runs at 5.1 TB/s.  What bounds the save beside memory is vector work: the magnitudes
 // are compared as packed 16-bit integers and the conversion divides by the scale
 // (with fp32 arithmetic for both: 11.6 us).
 constexpr int kSaveUnits = 2, kRestoreUnits = 4;
@@ -177,7 +178,8 @@ struct WeightParams {
 };
 
 // One workgroup per 128 x 128 block: 16 lanes x 8 values a row, 16 rows a
-// pass.  TR: the block's codes go through LDS and out as columns, so the
+// pass.  A stream over HBM: 14336 x 4096 bf16 in 34.4 us (5.1 TB/s), transposed
+// 37.4; fp32 53.7 and 56.5.  TR: the block's codes go through LDS and out as columns, so the
 // codes and scales are those of the transposed weight (a block's largest
 // magnitude is the same either way).
 constexpr int kTrPitch = kQBlock + 4;
