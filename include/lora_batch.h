@@ -32,7 +32,8 @@
  *     ldx elements; y is [T, d_out] with pitch ldy.
  *   - Element type (lora_dtype) applies to x, y, dY, dX, A_a and B_a.  v, g,
  *     dA and dB are always fp32.  bf16 results (y, dX) are formed in fp32 and
- *     rounded once, to nearest even.
+ *     rounded once, to nearest even (lora_base_product: of products that its
+ *     matrix instruction cuts, as stated there).
  *   - All data pointers are DEVICE pointers unless stated; the lora_segments
  *     struct itself is passed by value from the host and holds device
  *     pointers.  `stream` is a hipStream_t (NULL = the null stream).  Every
