@@ -19,6 +19,22 @@ block of 128):
     y = lora_base_product(xq, wq)                        # y = W x
     lora_base_product(lora_quant_rows(dy), wt, y=dx)     # dX = W^T dY
     lora_backward_quant(xq[s:e], dy, table, grads, seg_ft, dx)   # dX, dA, dB from the saved rows
+
+A frozen weight in microscaled 4 bits (e2m1 codes, one power-of-two scale per 32
+columns), for rows in 8 or 4 bits:
+
+    w4 = lora_quant_rows_mx(W).as_weight()               # forward alone: a scale for each row's 32 columns
+    w4, wt4 = lora_quant_weight_mx(W), lora_quant_weight_mx(W, transpose=True)   # the same values in both
+    y = lora_base_product_mx(xq, w4)                     # y = W x
+
+A mixture of experts: every token's rows to its k experts and back:
+
+    seg = lora_expert_segments(expert_ids, num_experts)  # [T, k] choices, sorted by expert
+    rows = lora_expert_gather(x, seg)                    # [T k, d]
+    out = lora_expert_product_mx(lora_quant_rows(rows), w4, seg)   # each expert's rows through its weight
+    y = lora_expert_combine(out, router_weights, seg)    # y[t] = sum_j w[t, j] out[pos[t, j]]
+    d_out, dw = lora_expert_combine_backward(dy, out, router_weights, seg)
+    dx = lora_expert_gather_backward(d_rows, seg)
 """
 from __future__ import annotations
 
@@ -39,6 +55,9 @@ __all__ = [
     "lora_abi_version", "lora_status_string", "LORA_BASE_PRODUCT_MAX_WORKSPACE",
     "lora_segments_workspace_bytes", "lora_shrink_workspace_bytes", "lora_backward_workspace_bytes",
     "lora_segments_sched_elems", "lora_base_product_workspace_bytes", "lora_backward_quant_workspace_bytes",
+    "MxRows", "MxWeight", "ExpertSegments", "lora_quant_rows_mx", "lora_dequant_rows_mx", "lora_quant_weight_mx",
+    "lora_base_product_mx", "lora_base_product_mx_workspace_bytes", "lora_expert_segments", "lora_expert_gather",
+    "lora_expert_gather_backward", "lora_expert_combine", "lora_expert_combine_backward", "lora_expert_product_mx",
 ]
 
 _DTYPES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
@@ -286,6 +305,80 @@ class QuantWeight(_Quant):
         self.d_out, self.d_in = int(d_out), int(d_in)
 
 
+class _Mx:
+    """Matrix in microscaled 4 bits: value = code * 2^(scale - 127), one scale per row and 32 columns.
+
+    codes: uint8 [rows, >= round_up(cols, 256) / 2], two e2m1 codes a byte (column 2 i in the low four bits),
+    scales: uint8 [rows, >= round_up(cols, 256) / 32], on one GPU with contiguous rows; row pitches multiples of
+    128 and 8.  Codes past the last column are zeros, scales of blocks without a column 127."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
+        if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("codes and scales must be uint8")
+        _on_gpu(codes, scales)
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must live on one device")
+        pad = -(-cols // _abi.LORA_MX_PAD) * _abi.LORA_MX_PAD
+        for name, t, c, unit in (("codes", codes, pad // 2, _abi.LORA_MX_PAD // 2),
+                                 ("scales", scales, pad // _abi.LORA_MX_BLOCK, _abi.LORA_MX_PAD // _abi.LORA_MX_BLOCK)):
+            if t.dim() != 2 or t.stride(1) != 1 or t.shape[0] != rows or t.shape[1] < c:
+                raise ValueError(f"{name} must be [{rows}, >= {c}] with contiguous rows")
+            if rows > 1 and (t.stride(0) % unit or t.stride(0) < t.shape[1]):
+                raise ValueError(f"the row pitch of {name} must be a multiple of {unit}")
+        self.codes, self.scales, self.device = codes, scales, codes.device
+        # (one row has no pitch: a slice of a wider matrix may stand at any, its own width is what counts)
+        self.c = _abi.LoraQuant(codes.data_ptr(), codes.stride(0) if rows > 1 else pad // 2,
+                                scales.data_ptr(), scales.stride(0) if rows > 1 else pad // _abi.LORA_MX_BLOCK)
+
+    @staticmethod
+    def _buffers(rows: int, cols: int, device):
+        pad = -(-cols // _abi.LORA_MX_PAD) * _abi.LORA_MX_PAD
+        u8 = dict(dtype=torch.uint8, device=device)
+        return torch.empty(rows, pad // 2, **u8), torch.empty(rows, pad // _abi.LORA_MX_BLOCK, **u8)
+
+
+class MxRows(_Mx):
+    """Rows [T, d] in microscaled 4 bits.  A slice of rows (q[a:b]) is a MxRows over the same memory."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, d: int):
+        self.T, self.d = int(codes.shape[0]), int(d)
+        super().__init__(codes, scales, self.T, self.d)
+
+    @classmethod
+    def empty(cls, T: int, d: int, device) -> "MxRows":
+        """Buffers for T rows of d values, contents unset (filled piece by piece)."""
+        return cls(*cls._buffers(T, d, device), d)
+
+    def as_weight(self, experts: Optional[int] = None) -> "MxWeight":
+        """These rows as a weight [T, d], or as `experts` weights [T / experts, d], one below the other."""
+        if self.T % (experts or 1):
+            raise ValueError(f"{self.T} rows are not {experts} weights")
+        return MxWeight(self.codes, self.scales, self.T // (experts or 1), self.d, experts)
+
+    def __len__(self) -> int:
+        return self.T
+
+    def __getitem__(self, rows: slice) -> "MxRows":
+        if not isinstance(rows, slice) or rows.step not in (None, 1):
+            raise TypeError("rows are taken as a slice of consecutive rows")
+        return MxRows(self.codes[rows], self.scales[rows], self.d)
+
+
+class MxWeight(_Mx):
+    """A weight [d_out, d_in] in microscaled 4 bits, or `experts` of them, one below the other: codes and scales have
+    experts * d_out rows."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, d_out: int, d_in: int, experts: Optional[int] = None):
+        if experts is not None and experts < 1:
+            raise ValueError("experts must be 1 or more")
+        super().__init__(codes, scales, d_out * (experts or 1), d_in)
+        self.d_out, self.d_in, self.experts = int(d_out), int(d_in), experts
+
+    def rows(self) -> MxRows:
+        """The weight's rows, of all experts, e.g. to restore them (lora_dequant_rows_mx)."""
+        return MxRows(self.codes, self.scales, self.d_in)
+
+
 class Segments:
     """Output of lora_segments_build: rows grouped by adapter (device tensors)."""
 
@@ -308,6 +401,18 @@ class Segments:
     def c(self) -> _abi.LoraSegments:
         """The C struct of device pointers (the tensors are allocated once, so it is built once)."""
         return self._c
+
+
+class ExpertSegments(Segments):
+    """Output of lora_expert_segments: the tokens' choices grouped by expert (Segments of tokens * k rows), and pos
+    [tokens, k], the place of every choice among the sorted rows (-1: of no expert)."""
+
+    def __init__(self, tokens: int, k: int, num_experts: int, device: torch.device):
+        super().__init__(tokens * k, num_experts, device)
+        self.tokens, self.k = tokens, k
+        self.pos = torch.full((tokens, k), -1, dtype=torch.int32, device=device)
+        self.device = self.pos.device
+        self._pos = self.pos.data_ptr()
 
 
 def lora_segments_build(adapter_ids: torch.Tensor, num_adapters: int, out: Optional[Segments] = None) -> Segments:
@@ -654,6 +759,237 @@ def lora_base_product(x: QuantRows, w: QuantWeight, y: Optional[torch.Tensor] = 
 
 def lora_backward_quant_workspace_bytes(dtype: torch.dtype, T_ft: int, d_in: int, d_out: int, r_max: int) -> int:
     return _abi.load().lora_backward_quant_workspace_bytes(_DTYPES[dtype], T_ft, d_in, d_out, r_max)
+
+
+def lora_quant_rows_mx(x: torch.Tensor, out: Optional[MxRows] = None) -> MxRows:
+    """Save rows x [T, d] (bfloat16 or float32) in microscaled 4 bits; out: buffers to fill (MxRows.empty, or a slice)."""
+    _on_gpu(x)
+    code, dev = _dtype_code(x), x.device
+    px, T, d, ldx = _rows(x, "x")
+    if out is None:
+        out = MxRows.empty(T, d, dev)
+    elif not isinstance(out, MxRows):
+        raise TypeError("out must be a MxRows")
+    elif out.T != T or out.d != d or out.device != dev:
+        raise ValueError(f"out must hold {T} rows of {d} values on x's device")
+    _abi.check("lora_quant_rows_mx", _launch(dev, _abi.load().lora_quant_rows_mx, code, px, ldx, T, d, out.c))
+    return out
+
+
+def lora_dequant_rows_mx(q, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of q (MxRows, or a MxWeight's rows), as a tensor of dtype (or into out, whose type counts)."""
+    if isinstance(q, MxWeight):
+        T, d = q.d_out * (q.experts or 1), q.d_in
+    elif isinstance(q, MxRows):
+        T, d = q.T, q.d
+    else:
+        raise TypeError("q must be a MxRows or a MxWeight")
+    dev = q.device
+    if out is None:
+        out = torch.empty(T, d, dtype=dtype, device=dev)
+    _on_gpu(out)
+    code = _dtype_code(out)
+    px, rows, cols, ldx = _rows(out, "out")
+    if rows != T or cols != d or out.device != dev:
+        raise ValueError(f"out must be [{T}, {d}] on q's device")
+    _abi.check("lora_dequant_rows_mx", _launch(dev, _abi.load().lora_dequant_rows_mx, code, q.c, T, d, px, ldx))
+    return out
+
+
+def lora_quant_weight_mx(w: torch.Tensor, transpose: bool = False, out: Optional[MxWeight] = None) -> MxWeight:
+    """A frozen weight [d_out, d_in], or the weights [experts, d_out, d_in], in microscaled 4 bits with a scale for
+    32 x 32 values; transpose: the form of the transpose, with the same values."""
+    _on_gpu(w)
+    code, dev = _dtype_code(w), w.device
+    experts = w.shape[0] if w.dim() == 3 else None
+    parts = w.unbind(0) if experts is not None else (w,)
+    if not parts:
+        raise ValueError("w holds no weight")
+    _, d_out, d_in, _ = _rows(parts[0], "w")
+    rows, cols = (d_in, d_out) if transpose else (d_out, d_in)
+    if out is None:
+        out = MxWeight(*MxWeight._buffers(rows * len(parts), cols, dev), rows, cols, experts)
+    elif not isinstance(out, MxWeight):
+        raise TypeError("out must be a MxWeight")
+    elif out.d_out != rows or out.d_in != cols or (out.experts or 1) != len(parts) or out.device != dev:
+        raise ValueError(f"out must hold {len(parts)} [{rows}, {cols}] weights on w's device")
+    lib = _abi.load()
+    q = out.c
+    for e, part in enumerate(parts):
+        pw, _, _, ldw = _rows(part, "w")
+        c = _abi.LoraQuant(q.codes + e * rows * q.ld, q.ld, q.scales + e * rows * q.lds, q.lds)
+        st = _launch(dev, lib.lora_quant_weight_mx, code, pw, ldw, d_out, d_in, int(bool(transpose)), c)
+        _abi.check("lora_quant_weight_mx", st)
+    return out
+
+
+def lora_base_product_mx_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
+    """Not monotone in T; never more than LORA_BASE_PRODUCT_MAX_WORKSPACE (128 MiB)."""
+    return _abi.load().lora_base_product_mx_workspace_bytes(T, d_in, d_out)
+
+
+def _mx_operands(fn: str, x, w, y, T_y, accumulate: bool, dtype):
+    """Checked (x_bits, y) of a product of rows x (MxRows or QuantRows) and a 4-bit weight w."""
+    if not isinstance(x, (MxRows, QuantRows)) or not isinstance(w, MxWeight):
+        raise TypeError(f"{fn}: x must be a MxRows or a QuantRows and w a MxWeight")
+    dev = x.device
+    if x.d != w.d_in or dev != w.device:
+        raise ValueError(f"{fn}: x has {x.d} columns on {dev}, w has d_in = {w.d_in} on {w.device}")
+    if y is None:
+        if accumulate:
+            raise ValueError(f"{fn}: accumulate needs y")
+        y = (torch.zeros if T_y is not None else torch.empty)(x.T, w.d_out, dtype=dtype, device=dev)
+    _on_gpu(y)
+    return 4 if isinstance(x, MxRows) else 8, y
+
+
+def lora_base_product_mx(x, w: MxWeight, y: Optional[torch.Tensor] = None, accumulate: bool = False,
+                         dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = W x for every row (accumulate: y += W x) with a 4-bit weight; x: MxRows (4 bits) or QuantRows (8 bits);
+    without y, a new tensor [T, d_out] of dtype.
+
+    Sums are fp32, rounded once.  Products are exact but for 8-bit rows with bfloat16 y, where the matrix instruction
+    cuts them as in lora_base_product."""
+    bits, y = _mx_operands("lora_base_product_mx", x, w, y, None, accumulate, dtype)
+    if w.experts is not None:
+        raise ValueError("lora_base_product_mx: w holds several experts' weights (lora_expert_product_mx)")
+    dev = x.device
+    code = _dtype_code(y)
+    py, T, d_out, ldy = _rows(y, "y")
+    if T != x.T or d_out != w.d_out or y.device != dev:
+        raise ValueError(f"y must be [{x.T}, {w.d_out}] on x's device")
+    lib = _abi.load()
+    if ws is None:  # a caller's workspace is size-checked by the library (LORA_ERR_WORKSPACE)
+        ws = torch.empty(max(lib.lora_base_product_mx_workspace_bytes(T, x.d, d_out), 1), dtype=torch.uint8, device=dev)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous on x's device")
+    st = _launch(dev, lib.lora_base_product_mx, code, bits, x.c, T, x.d, w.c, d_out, py, ldy, 1 if accumulate else 0,
+                 ws.data_ptr(), ws.nbytes)
+    _abi.check("lora_base_product_mx", st)
+    return y
+
+
+def lora_expert_segments(expert_ids: torch.Tensor, num_experts: int, out: Optional[ExpertSegments] = None) -> ExpertSegments:
+    """Group the choices expert_ids [tokens, k] (int32, -1 = none) by expert.  Returns (or refills) an ExpertSegments."""
+    _on_gpu(expert_ids)
+    if expert_ids.dtype != torch.int32 or expert_ids.dim() != 2 or not expert_ids.is_contiguous():
+        raise ValueError("expert_ids must be a contiguous 2-D int32 tensor")
+    T, k = expert_ids.shape
+    dev = expert_ids.device
+    seg = out if out is not None else ExpertSegments(T, k, num_experts, dev)
+    if not isinstance(seg, ExpertSegments):
+        raise TypeError("out must be an ExpertSegments")
+    if seg.tokens != T or seg.k != k or seg.num_adapters != num_experts or seg.device != dev:
+        raise ValueError("ExpertSegments buffers were sized for another batch")
+    st = _launch(dev, _abi.load().lora_expert_segments, expert_ids.data_ptr(), T, k, num_experts, seg.c, seg._pos,
+                 seg.ws.data_ptr(), seg.ws.numel())
+    _abi.check("lora_expert_segments", st)
+    return seg
+
+
+def _expert_rows(fn: str, seg, t: torch.Tensor, name: str, rows: int, like: Optional[torch.Tensor] = None):
+    """Checked (pointer, columns, pitch) of a matrix with `rows` rows on the segments' device (and like's type and width)."""
+    if not isinstance(seg, ExpertSegments):
+        raise TypeError(f"{fn}: seg must be an ExpertSegments (lora_expert_segments)")
+    _on_gpu(t)
+    pt, n, d, ld = _rows(t, name)
+    if n != rows or t.device != seg.device:
+        raise ValueError(f"{fn}: {name} must have {rows} rows on the segments' device")
+    if like is not None and (t.dtype != like.dtype or d != like.shape[1]):
+        raise ValueError(f"{fn}: {name} must be {like.dtype} with {like.shape[1]} columns")
+    return pt, d, ld
+
+
+def _router_weights(fn: str, seg: ExpertSegments, w: torch.Tensor, name: str = "w") -> int:
+    if w.dtype != torch.float32 or w.dim() != 2 or w.shape != seg.pos.shape or not w.is_contiguous() or w.device != seg.device:
+        raise ValueError(f"{fn}: {name} must be float32 [{seg.tokens}, {seg.k}], contiguous, on the segments' device")
+    return w.data_ptr()
+
+
+def lora_expert_gather(x: torch.Tensor, seg: ExpertSegments, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[pos[t, j]] = x[t]: every token's row at the places of its choices, sorted by expert.  y [tokens * k, d]: rows
+    behind the last expert's are left as they are (zeros in a new y)."""
+    fn = "lora_expert_gather"
+    px, d, ldx = _expert_rows(fn, seg, x, "x", getattr(seg, "tokens", 0))
+    if y is None:
+        y = torch.zeros(seg.T, d, dtype=x.dtype, device=x.device)
+    py, _, ldy = _expert_rows(fn, seg, y, "y", seg.T, x)
+    _abi.check(fn, _launch(seg.device, _abi.load().lora_expert_gather, _dtype_code(x), px, ldx, seg.tokens, d, seg.k, seg._pos,
+                           py, ldy))
+    return y
+
+
+def lora_expert_gather_backward(dy: torch.Tensor, seg: ExpertSegments, dx: Optional[torch.Tensor] = None,
+                                accumulate: bool = False) -> torch.Tensor:
+    """The gather's gradient: dx[t] = sum_j dy[pos[t, j]] (accumulate: +=), in fp32, rounded once."""
+    fn = "lora_expert_gather_backward"
+    pdy, d, lddy = _expert_rows(fn, seg, dy, "dy", getattr(seg, "T", 0))
+    if dx is None:
+        if accumulate:
+            raise ValueError(f"{fn}: accumulate needs dx")
+        dx = torch.empty(seg.tokens, d, dtype=dy.dtype, device=dy.device)
+    pdx, _, lddx = _expert_rows(fn, seg, dx, "dx", seg.tokens, dy)
+    _abi.check(fn, _launch(seg.device, _abi.load().lora_expert_gather_backward, _dtype_code(dy), pdy, lddy, seg.tokens, d, seg.k,
+                           seg._pos, pdx, lddx, 1 if accumulate else 0))
+    return dx
+
+
+def lora_expert_combine(o: torch.Tensor, w: torch.Tensor, seg: ExpertSegments, y: Optional[torch.Tensor] = None,
+                        accumulate: bool = False) -> torch.Tensor:
+    """y[t] = sum_j w[t, j] o[pos[t, j]] (accumulate: +=), in fp32, rounded once; o [tokens * k, d] sorted by expert,
+    w [tokens, k] float32."""
+    fn = "lora_expert_combine"
+    po, d, ldo = _expert_rows(fn, seg, o, "o", getattr(seg, "T", 0))
+    pw = _router_weights(fn, seg, w)
+    if y is None:
+        if accumulate:
+            raise ValueError(f"{fn}: accumulate needs y")
+        y = torch.empty(seg.tokens, d, dtype=o.dtype, device=o.device)
+    py, _, ldy = _expert_rows(fn, seg, y, "y", seg.tokens, o)
+    _abi.check(fn, _launch(seg.device, _abi.load().lora_expert_combine, _dtype_code(o), po, ldo, seg.tokens, d, seg.k, seg._pos, pw,
+                           py, ldy, 1 if accumulate else 0))
+    return y
+
+
+def lora_expert_combine_backward(dy: torch.Tensor, o: torch.Tensor, w: torch.Tensor, seg: ExpertSegments,
+                                 d_o: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None):
+    """The combine's gradient: d_o[pos[t, j]] = w[t, j] dy[t] and dw[t, j] = <dy[t], o[pos[t, j]]> (float32; 0 for a
+    choice of no expert).  Returns (d_o, dw).  Rows of d_o behind the last expert's are left as they are (zeros in a
+    new d_o); d_o may be o."""
+    fn = "lora_expert_combine_backward"
+    pdy, d, lddy = _expert_rows(fn, seg, dy, "dy", getattr(seg, "tokens", 0))
+    po, _, ldo = _expert_rows(fn, seg, o, "o", seg.T, dy)
+    pw = _router_weights(fn, seg, w)
+    if d_o is None:
+        d_o = torch.zeros(seg.T, d, dtype=dy.dtype, device=dy.device)
+    if dw is None:
+        dw = torch.empty(seg.tokens, seg.k, dtype=torch.float32, device=dy.device)
+    pd, _, ldd = _expert_rows(fn, seg, d_o, "d_o", seg.T, dy)
+    _abi.check(fn, _launch(seg.device, _abi.load().lora_expert_combine_backward, _dtype_code(dy), pdy, lddy, po, ldo, seg.tokens, d,
+                           seg.k, seg._pos, pw, pd, ldd, _router_weights(fn, seg, dw, "dw")))
+    return d_o, dw
+
+
+def lora_expert_product_mx(x, w: MxWeight, seg: Segments, y: Optional[torch.Tensor] = None, accumulate: bool = False,
+                           dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """y[i] = W_e x[i] (accumulate: +=) for every sorted row i of expert e, each expert with its own 4-bit weight, in
+    one launch.  x: MxRows or QuantRows of the sorted rows; w: MxWeight with experts.  Rows behind the last expert's
+    are left as they are (zeros in a new y).  Precision: as lora_base_product_mx."""
+    fn = "lora_expert_product_mx"
+    if not isinstance(seg, Segments):
+        raise TypeError(f"{fn}: seg must be a Segments (lora_expert_segments)")
+    bits, y = _mx_operands(fn, x, w, y, seg.T, accumulate, dtype)
+    dev = x.device
+    code = _dtype_code(y)
+    py, T, d_out, ldy = _rows(y, "y")
+    if T != x.T or d_out != w.d_out or y.device != dev:
+        raise ValueError(f"{fn}: y must be [{x.T}, {w.d_out}] on x's device")
+    if seg.T != T or seg.num_adapters != (w.experts or 1) or seg.offsets.device != dev:
+        raise ValueError(f"{fn}: the segments are of {seg.T} rows and {seg.num_adapters} experts on {seg.offsets.device}, the call "
+                         f"has {T} and {w.experts or 1} on {dev}")
+    _abi.check(fn, _launch(dev, _abi.load().lora_expert_product_mx, code, bits, x.c, T, x.d, w.c, w.experts or 1, d_out, seg.c, py, ldy,
+                           1 if accumulate else 0))
+    return y
 
 
 def lora_adamw_step(tensors, *, step: int, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,

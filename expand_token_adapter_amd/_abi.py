@@ -67,6 +67,8 @@ LORA_MAX_SLICES = 3
 
 LORA_QUANT_BLOCK = 128
 LORA_BASE_PRODUCT_MAX_WORKSPACE = 128 << 20
+LORA_MX_BLOCK = 32
+LORA_MX_PAD = 256
 
 
 class LoraQuant(ctypes.Structure):
@@ -111,6 +113,20 @@ SIGNATURES = {
     "lora_backward_quant_workspace_bytes": (_sz, [ctypes.c_int, _i32, _i32, _i32, _i32]),
     "lora_backward_quant": (ctypes.c_int, [ctypes.c_int, LoraQuant, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp,
                                            _i32, _i32, LoraSegments, _vp, _i64, _vp, _sz, _vp]),
+    "lora_quant_rows_mx": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _i32, LoraQuant, _vp]),
+    "lora_dequant_rows_mx": (ctypes.c_int, [ctypes.c_int, LoraQuant, _i32, _i32, _vp, _i64, _vp]),
+    "lora_quant_weight_mx": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _i32, _i32, LoraQuant, _vp]),
+    "lora_base_product_mx_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "lora_base_product_mx": (ctypes.c_int, [ctypes.c_int, _i32, LoraQuant, _i32, _i32, LoraQuant, _i32, _vp, _i64, _i32,
+                                            _vp, _sz, _vp]),
+    "lora_expert_segments": (ctypes.c_int, [_vp, _i32, _i32, _i32, LoraSegments, _vp, _vp, _sz, _vp]),
+    "lora_expert_gather": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _vp]),
+    "lora_expert_gather_backward": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _i64, _i32, _vp]),
+    "lora_expert_combine": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _i32, _vp]),
+    "lora_expert_combine_backward": (ctypes.c_int, [ctypes.c_int, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp,
+                                                    _i64, _vp, _vp]),
+    "lora_expert_product_mx": (ctypes.c_int, [ctypes.c_int, _i32, LoraQuant, _i32, _i32, LoraQuant, _i32, _i32,
+                                              LoraSegments, _vp, _i64, _i32, _vp]),
 }
 
 _lib = None

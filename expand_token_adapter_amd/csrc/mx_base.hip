@@ -1,0 +1,143 @@
+// mx_base.hip -- lora_base_product_mx and lora_expert_product_mx (mx_plan.h chooses the
+// kernel).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "mx_base.h"
+
+using namespace lora;
+
+namespace {
+
+// WN x WT waves a workgroup
+template <int XB, int DT, int KIND, int WN, int WT>
+void launch_tiles(const MxParams& p, unsigned grid, hipStream_t st) {
+    constexpr MxTile c = kMxTiles[KIND];
+    static_assert(WN * WT * kWave <= c.threads, "the plan's bound on the launch");
+    hipLaunchKernelGGL((mx_kernel<c.bn, c.bt, WN, WT, XB == 4 ? c.stages4 : c.stages8, XB, DT>), dim3(grid), dim3(WN * WT * kWave), 0,
+                       st, p);
+}
+
+// tiles_t: tiles along t of all weights, at most
+template <int XB, int DT>
+int launch_mx(MxParams p, const BasePlan& b, int64_t tiles_t, hipStream_t st) {
+    p.splits = b.splits;
+    if (b.kind == kMxStream) {
+        p.tiles_n = (p.N + 15) / 16;
+        hipLaunchKernelGGL((mx_stream_kernel<kMxStreamWaves, XB, DT>), dim3((unsigned)(p.tiles_n * tiles_t)),
+                           dim3(kMxStreamWaves * kWave), 0, st, p);
+        return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+    }
+    const MxTile& c = kMxTiles[b.kind];
+    p.tiles_n = (p.N + c.bn - 1) / c.bn;
+    p.tiles_t = (int32_t)tiles_t;
+    const unsigned grid = (unsigned)round_up(p.tiles_n * tiles_t * p.splits, kNumXcd);
+    switch (b.kind) {
+        case kMx32x64: launch_tiles<XB, DT, kMx32x64, 1, 4>(p, grid, st); break;
+        case kMx64x64: launch_tiles<XB, DT, kMx64x64, 2, 2>(p, grid, st); break;
+        case kMx64x128: launch_tiles<XB, DT, kMx64x128, 2, 2>(p, grid, st); break;
+        case kMx128x128: launch_tiles<XB, DT, kMx128x128, 2, 2>(p, grid, st); break;
+        case kMx256x128: launch_tiles<XB, DT, kMx256x128, 2, 2>(p, grid, st); break;
+        default: launch_tiles<XB, DT, kMx256x256, 2, 4>(p, grid, st); break;
+    }
+    if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
+    if (p.splits > 1) {
+        BaseParams q{};
+        q.y = p.y;
+        q.ldy = p.ldy;
+        q.T = p.T;
+        q.N = p.N;
+        q.accumulate = p.accumulate;
+        q.splits = p.splits;
+        q.part = p.part;
+        const int64_t n = (int64_t)p.T * (p.N / 4);
+        const unsigned sum_grid = (unsigned)std::min<int64_t>((n + kSumThreads - 1) / kSumThreads, kCus * 8);
+        hipLaunchKernelGGL(base_sum_kernel<DT>, dim3(sum_grid), dim3(kSumThreads), 0, st, q);
+    }
+    return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
+int launch(const MxParams& p, int bits, int dtype, const BasePlan& b, int64_t tiles_t, void* stream) {
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (bits == 4) return dtype == LORA_BF16 ? launch_mx<4, LORA_BF16>(p, b, tiles_t, st) : launch_mx<4, LORA_F32>(p, b, tiles_t, st);
+    return dtype == LORA_BF16 ? launch_mx<8, LORA_BF16>(p, b, tiles_t, st) : launch_mx<8, LORA_F32>(p, b, tiles_t, st);
+}
+
+// What both products check; d_out: of one weight.
+int check_product(int dtype, int32_t bits, const lora_quant& x, int32_t T, int32_t d_in, const lora_quant& w, int32_t d_out, const void* y,
+                  int64_t ldy) {
+    int rc = bits == 4 ? check_mx(x, d_in) : check_quant(x, d_in);
+    if (rc == LORA_OK) rc = check_mx(w, d_in);
+    if (rc == LORA_OK) rc = check_matrix(y, d_out, ldy);
+    if (rc != LORA_OK) return rc;
+    // a tile's 256 rows are addressed with 32-bit byte offsets, rows and outputs numbered in 32 bits
+    if (x.ld > LORA_QUANT_MAX_LD || w.ld > LORA_QUANT_MAX_LD || x.lds > LORA_QUANT_MAX_LD || w.lds > LORA_QUANT_MAX_LD ||
+        T > INT32_MAX - 256 || d_out > INT32_MAX - 256)
+        return LORA_ERR_UNSUPPORTED;
+    return LORA_OK;
+}
+bool valid_product(int dtype, int32_t bits, int32_t T, int32_t d_in, int32_t d_out, int32_t accumulate) {
+    return valid_dtype(dtype) && (bits == 4 || bits == 8) && T >= 0 && d_in >= 1 && d_out >= 1 && (accumulate == 0 || accumulate == 1);
+}
+MxParams product_params(int32_t bits, const lora_quant& x, int32_t T, int32_t d_in, const lora_quant& w, int32_t d_out, void* y,
+                        int64_t ldy, int32_t accumulate) {
+    MxParams p{};
+    p.x = x.codes;
+    p.ldx = x.ld;
+    p.xs = x.scales;
+    p.ldxs = x.lds;
+    p.w = w.codes;
+    p.ldw = w.ld;
+    p.ws = w.scales;
+    p.ldws = w.lds;
+    p.y = static_cast<char*>(y);
+    p.ldy = ldy;
+    p.T = T;
+    p.N = d_out;
+    p.steps = (int32_t)(((int64_t)d_in + mx_step(bits) - 1) / mx_step(bits));
+    p.accumulate = accumulate;
+    return p;
+}
+
+}  // namespace
+
+extern "C" size_t lora_base_product_mx_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out) {
+    if (T < 0 || d_in < 1 || d_out < 1) return 0;
+    if (T == 0) return 16;
+    size_t most = 0;
+    for (const int bits : {4, 8})
+        for (const int dtype : {LORA_BF16, LORA_F32})
+            most = std::max(most, base_workspace_bytes(mx_plan(bits, dtype, T, d_in, d_out), T, d_out));
+    return most;
+}
+
+extern "C" int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
+                                    int64_t ldy, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+    if (!valid_product(dtype, x_bits, T, d_in, d_out, accumulate)) return LORA_ERR_INVALID_ARG;
+    if (T == 0) return LORA_OK;
+    const int rc = check_product(dtype, x_bits, x, T, d_in, w, d_out, y, ldy);
+    if (rc != LORA_OK) return rc;
+    const BasePlan b = mx_plan(x_bits, dtype, T, d_in, d_out);
+    if (b.kind == kMxKinds) return LORA_ERR_UNSUPPORTED;
+    if (!ws || !aligned16(ws) || ws_bytes < base_workspace_bytes(b, T, d_out)) return LORA_ERR_WORKSPACE;
+    MxParams p = product_params(x_bits, x, T, d_in, w, d_out, y, ldy, accumulate);
+    p.part = static_cast<float*>(ws);
+    return launch(p, x_bits, dtype, b, b.kind == kMxStream ? 1 : (T + kMxTiles[b.kind].bt - 1) / kMxTiles[b.kind].bt, stream);
+}
+
+extern "C" int lora_expert_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t num_experts,
+                                      int32_t d_out, lora_segments seg, void* y, int64_t ldy, int32_t accumulate, void* stream) {
+    if (!valid_product(dtype, x_bits, T, d_in, d_out, accumulate) || num_experts < 1) return LORA_ERR_INVALID_ARG;
+    if (T == 0) return LORA_OK;
+    if (!seg.offsets) return LORA_ERR_INVALID_ARG;
+    const int rc = check_product(dtype, x_bits, x, T, d_in, w, d_out, y, ldy);
+    if (rc != LORA_OK) return rc;
+    int64_t tiles_t = 0;
+    const BasePlan b = mx_expert_plan(x_bits, dtype, T, d_in, d_out, num_experts, &tiles_t);
+    if (b.kind == kMxKinds) return LORA_ERR_UNSUPPORTED;
+    MxParams p = product_params(x_bits, x, T, d_in, w, d_out, y, ldy, accumulate);
+    p.offsets = seg.offsets;
+    p.experts = num_experts;
+    return launch(p, x_bits, dtype, b, tiles_t, stream);
+}

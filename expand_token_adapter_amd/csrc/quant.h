@@ -34,6 +34,26 @@ __device__ __forceinline__ uint32_t quant_scale_byte(uint32_t top) {
 // (checked for every byte and code).
 __device__ __forceinline__ float quant_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+// ------------------------------------------------------------------ magnitudes
+
+// fp32 bits of the largest magnitude of 8 values, at or above kNotFinite if one
+// of them is not finite.
+constexpr uint32_t kNotFinite = 0x7f800000u;
+__device__ __forceinline__ uint32_t max8(const Frag<LORA_BF16>& f) {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t top{0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2_t, f.q[i] & 0x7fff7fffu));
+    return (uint32_t)max(top[0], top[1]) << 16;
+}
+__device__ __forceinline__ uint32_t max8(const Frag<LORA_F32>& f) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(f.q0[i] & 0x7fffffffu, f.q1[i] & 0x7fffffffu));
+    return top;
+}
+
 // ------------------------------------------------------------------ codes
 
 // 8 codes times a scale, as an operand fragment (bf16: exact for scale bytes

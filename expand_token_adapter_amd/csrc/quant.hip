@@ -23,24 +23,6 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
     return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x121, 0xf, 0xf, true));
 }
 
-// fp32 bits of the largest magnitude of 8 values, at or above kNotFinite if one
-// of them is not finite.
-constexpr uint32_t kNotFinite = 0x7f800000u;
-__device__ __forceinline__ uint32_t max8(const Frag<LORA_BF16>& f) {
-    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-    u16x2_t top{0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2_t, f.q[i] & 0x7fff7fffu));
-    return (uint32_t)max(top[0], top[1]) << 16;
-}
-__device__ __forceinline__ uint32_t max8(const Frag<LORA_F32>& f) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(f.q0[i] & 0x7fffffffu, f.q1[i] & 0x7fffffffu));
-    return top;
-}
-
 // The 8 values with zeros (nan false) or NaN in place of those that are not finite.
 template <int DT>
 __device__ Frag<DT> finite8(const Frag<DT>& f, bool nan) {

@@ -166,15 +166,20 @@ __global__ __launch_bounds__(kChunk) void seg_scatter_kernel(const int32_t* __re
                                                              const int32_t* __restrict__ pre16,
                                                              const int32_t* __restrict__ pre64,
                                                              int32_t* __restrict__ perm, int32_t* __restrict__ sched,
-                                                             int64_t tiles16_off, int64_t tiles64_off) {
+                                                             int64_t tiles16_off, int64_t tiles64_off,
+                                                             int32_t* __restrict__ place) {
     const int c = blockIdx.x;
     const int64_t t = (int64_t)c * kChunk + threadIdx.x;
     if (t >= T) return;
     const int32_t id = ids[t];
-    if (id < 0 || id >= A) return;
+    if (id < 0 || id >= A) {
+        if (place) place[t] = -1;
+        return;
+    }
     const int32_t local = hist[(int64_t)id * nchunks + c] + rank[t];  // position inside the adapter's group
     const int32_t pos = offsets[id] + local;
     perm[pos] = (int32_t)t;
+    if (place) place[t] = pos;
     const int32_t cnt = counts[id];
     if ((local & 15) == 0) {
         int32_t* rec = sched + tiles16_off + 4 * (int64_t)(pre16[id] + local / 16);
@@ -279,12 +284,14 @@ struct SegSmallJob {
     int32_t* sched;
     int32_t* err;
     int64_t active_off, tiles16_off, tiles64_off;
+    int32_t* place;  // (PLACE) every row's sorted position, -1 for none
 };
 constexpr int kSegBatchMax = LORA_SEG_BATCH_MAX;
 struct SegSmallJobs {
     SegSmallJob job[kSegBatchMax];
 };
 
+template <bool PLACE>
 __global__ __launch_bounds__(kScanThreads) void seg_small_kernel(SegSmallJobs jobs, int32_t A) {
     const SegSmallJob& job = jobs.job[blockIdx.x];
     const int32_t* __restrict__ ids = job.ids;
@@ -416,6 +423,7 @@ __global__ __launch_bounds__(kScanThreads) void seg_small_kernel(SegSmallJobs jo
                 const int pos = info.x + local;
                 const int cnt = info.y;
                 perm[pos] = t;
+                if constexpr (PLACE) job.place[t] = pos;
                 if ((local & 15) == 0) {
                     const int rows = cnt - local < 16 ? cnt - local : 16;
                     *reinterpret_cast<int4*>(sched + tiles16_off + 4 * (int64_t)(info.z + local / 16)) =
@@ -426,6 +434,8 @@ __global__ __launch_bounds__(kScanThreads) void seg_small_kernel(SegSmallJobs jo
                     *reinterpret_cast<int4*>(sched + tiles64_off + 4 * (int64_t)(info.w + local / 64)) =
                         make_int4(id, pos, rows, 0);
                 }
+            } else if (PLACE && t < r1) {
+                job.place[t] = -1;
             }
             // every lane has read its cursor: the lowest lane of each id advances it
             __builtin_amdgcn_wave_barrier();
@@ -466,14 +476,15 @@ int seg_check(const int32_t* adapter_ids, int32_t T, int32_t num_adapters, const
     return LORA_OK;
 }
 bool seg_small(int32_t T, int32_t num_adapters) { return T <= kSmallMaxT && num_adapters <= kSmallMaxA; }
-SegSmallJob small_job(const int32_t* adapter_ids, int32_t T, int32_t num_adapters, const lora_segments& seg) {
+SegSmallJob small_job(const int32_t* adapter_ids, int32_t T, int32_t num_adapters, const lora_segments& seg,
+                      int32_t* place = nullptr) {
     const SchedLayout sl = SchedLayout::make(T, num_adapters);
     return SegSmallJob{adapter_ids, T, seg.counts, seg.offsets, seg.perm, seg.sched, seg.err,
-                       sl.active, sl.tiles16, sl.tiles64};
+                       sl.active, sl.tiles16, sl.tiles64, place};
 }
 // The three-kernel path for batches beyond the one-workgroup limits.
 void seg_large(const int32_t* adapter_ids, int32_t T, int32_t num_adapters, const lora_segments& seg, void* ws,
-               hipStream_t st) {
+               hipStream_t st, int32_t* place = nullptr) {
     const SegWs w = SegWs::make(T, num_adapters);
     const int32_t nchunks = (int32_t)(((int64_t)T + kChunk - 1) / kChunk);
     const SchedLayout sl = SchedLayout::make(T, num_adapters);
@@ -485,7 +496,7 @@ void seg_large(const int32_t* adapter_ids, int32_t T, int32_t num_adapters, cons
                        sl.active);
     hipLaunchKernelGGL(seg_scatter_kernel, dim3(nchunks), dim3(kChunk), 0, st, adapter_ids, T, num_adapters, nchunks,
                        wsi + w.hist, wsi + w.rank, seg.counts, seg.offsets, wsi + w.pre16, wsi + w.pre64, seg.perm,
-                       seg.sched, sl.tiles16, sl.tiles64);
+                       seg.sched, sl.tiles16, sl.tiles64, place);
 }
 }  // namespace
 
@@ -497,7 +508,7 @@ extern "C" int lora_segments_build(const int32_t* adapter_ids, int32_t T, int32_
     if (seg_small(T, num_adapters)) {
         SegSmallJobs jobs{};
         jobs.job[0] = small_job(adapter_ids, T, num_adapters, seg);
-        hipLaunchKernelGGL(seg_small_kernel, dim3(1), dim3(kScanThreads), 0, st, jobs, num_adapters);
+        hipLaunchKernelGGL(seg_small_kernel<false>, dim3(1), dim3(kScanThreads), 0, st, jobs, num_adapters);
     } else {
         seg_large(adapter_ids, T, num_adapters, seg, ws, st);
     }
@@ -517,7 +528,7 @@ extern "C" int lora_segments_build_batch(const lora_segments_job* jobs, int32_t 
     SegSmallJobs batch{};
     int nb = 0;
     auto flush = [&]() {
-        if (nb > 0) hipLaunchKernelGGL(seg_small_kernel, dim3(nb), dim3(kScanThreads), 0, st, batch, num_adapters);
+        if (nb > 0) hipLaunchKernelGGL(seg_small_kernel<false>, dim3(nb), dim3(kScanThreads), 0, st, batch, num_adapters);
         nb = 0;
     };
     for (int32_t i = 0; i < n_jobs; ++i) {
@@ -531,5 +542,23 @@ extern "C" int lora_segments_build_batch(const lora_segments_job* jobs, int32_t 
         }
     }
     flush();
+    return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
+extern "C" int lora_expert_segments(const int32_t* expert_ids, int32_t T, int32_t k, int32_t num_experts, lora_segments seg, int32_t* pos,
+                                    void* ws, size_t ws_bytes, void* stream) {
+    if (T < 0 || k < 1 || (int64_t)T * k > INT32_MAX) return LORA_ERR_INVALID_ARG;
+    const int32_t rows = T * k;
+    const int rc = seg_check(expert_ids, rows, num_experts, seg, ws, ws_bytes);
+    if (rc != LORA_OK || T == 0) return rc;
+    if (!pos || ((uintptr_t)pos & 3u)) return LORA_ERR_INVALID_ARG;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (seg_small(rows, num_experts)) {
+        SegSmallJobs jobs{};
+        jobs.job[0] = small_job(expert_ids, rows, num_experts, seg, pos);
+        hipLaunchKernelGGL(seg_small_kernel<true>, dim3(1), dim3(kScanThreads), 0, st, jobs, num_experts);
+    } else {
+        seg_large(expert_ids, rows, num_experts, seg, ws, st, pos);
+    }
     return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }

@@ -553,6 +553,152 @@ int lora_backward_quant(int dtype, lora_quant x, const void* dy, int64_t lddy, v
                         int32_t num_adapters, int32_t r_max, lora_segments seg_ft, const float* v_saved, int64_t ldv,
                         void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ microscaled 4-bit rows and weights
+ *
+ * A frozen base weight in half the bytes of the 8-bit form, and rows for its
+ * products.  The mx form of a matrix of rows x cols values is a lora_quant with
+ *     value[i][j] = code[i][j] * 2^(scale - 127)
+ *   codes  [rows, ld]  two e2m1 codes a byte, column 2 i in the low four bits (1
+ *          sign, 2 exponent, 1 fraction bits, bias 1: 0, 0.5, 1, 1.5, 2, 3, 4, 6);
+ *          16-byte aligned; ld counts BYTES, >= round_up(cols, 256) / 2 and a
+ *          multiple of 128.
+ *   scales [rows, lds] one exponent byte per row and 32 columns (255 is NaN),
+ *          8-byte aligned, lds >= round_up(cols, 256) / 32 and a multiple of 8.
+ *   Columns cols .. round_up(cols, 256) - 1 hold codes of zero, and scale bytes of
+ *   blocks without a column are 127: the calls that write the form write them, and
+ *   the calls that read it rely on it.
+ *   cols a multiple of 8.
+ * A block's scale is the smallest power of two, 2^-127 at the least, that brings
+ * its largest magnitude to 6 or less (1 for a block of zeros); codes are rounded to
+ * nearest, ties to even.  A block with a value that is not finite becomes NaN as a
+ * whole (scale 255, codes of zero).
+ */
+#define LORA_MX_BLOCK 32
+#define LORA_MX_PAD 256
+
+/*
+ * Save rows: q = the mx form of x [T, ldx] (dtype), d columns, a scale for each row
+ * and 32 columns.  One kernel.  A range of a longer matrix is saved by pointer
+ * offsets of x and q.  LORA_ERR_UNSUPPORTED for more than 2^29 - 64 units of 256
+ * columns: save pieces.
+ */
+int lora_quant_rows_mx(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, lora_quant q, void* stream);
+
+/*
+ * Restore rows: x [T, ldx] (dtype) = the values of q, d columns (exact in both
+ * types; magnitudes from 2^128 up, which start at scale byte 253 and come from saved
+ * ones of 1.75 * 2^127 or more, are infinite).  One kernel.  LORA_ERR_UNSUPPORTED as
+ * lora_quant_rows_mx.
+ */
+int lora_dequant_rows_mx(int dtype, lora_quant q, int32_t T, int32_t d, void* x, int64_t ldx, void* stream);
+
+/*
+ * mx form of a weight w [d_out, ldw] (dtype, d_in columns) whose 32 x 32 blocks share
+ * a scale (stored for each of the block's rows), so that both forms hold the same
+ * values: transpose = 0: q is [d_out, d_in]; transpose = 1: q is the transposed
+ * weight [d_in, d_out], for products with W^T (dX = W^T dY).  A weight that is used
+ * in one direction alone is better saved by lora_quant_rows_mx, with a scale of its
+ * own for each row.  d_out and d_in multiples of 8.  One kernel, once per weight.
+ * LORA_ERR_UNSUPPORTED for d_out above 32 * 65535 (transpose = 1: d_in above 64 *
+ * 65535) and rows of more than 2^24 - 1 units of 256 columns.
+ */
+int lora_quant_weight_mx(int dtype, const void* w, int64_t ldw, int32_t d_out, int32_t d_in, int32_t transpose,
+                         lora_quant q, void* stream);
+
+/* Workspace bytes of lora_base_product_mx for rows in 4 or 8 bits and either dtype
+ * (host, pure).  More rows may need less; no call needs more than
+ * LORA_BASE_PRODUCT_MAX_WORKSPACE. */
+size_t lora_base_product_mx_workspace_bytes(int32_t T, int32_t d_in, int32_t d_out);
+
+/*
+ * lora_base_product with a 4-bit weight: y_t = W x_t (accumulate = 0) or y_t += W x_t
+ * (accumulate = 1) for every row of x.
+ *   x: rows [T, d_in] in the mx form (x_bits = 4) or in the 8-bit form of
+ *   lora_quant_rows (x_bits = 8); w: mx form of the weight [d_out, d_in]; y [T, ldy]
+ *   (dtype).  The sums (and y_t before, if added to) are fp32 and rounded once to y's
+ *   type.  What they sum:
+ *   x_bits = 4  exact products, for either dtype.
+ *   x_bits = 8  LORA_F32: exact products of the values as bf16 numbers (for the 8-bit
+ *          rows' scale bytes from 3 to 246; as in lora_base_product).  LORA_BF16:
+ *          products cut as in lora_base_product, each of the 8 of columns 8 i ..
+ *          8 i + 7 below 2^-13 of the power of two of the largest, with W_k =
+ *          max(|w_k|, s) in its bound (0 for w_k = 0), s the scale of w_k's block.
+ *   ws: lora_base_product_mx_workspace_bytes(T, d_in, d_out) bytes.
+ * Rows are independent, and the order of every sum is fixed by the shapes, as in
+ * lora_base_product, and so are its refusals (pitches of scales included).
+ */
+int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
+                         int64_t ldy, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ mixture of experts
+ *
+ * A base layer may hold several weights, experts, of which every token chooses k.
+ * Its T k choices (choice j of token t is number t k + j) are grouped by expert as
+ * rows are by adapter; the rows that go through the experts lie sorted, expert e's
+ * at seg.offsets[e] .. seg.offsets[e + 1] - 1.  Adapters of the sorted rows are
+ * applied as of any rows (lora_segments_build over the sorted rows' adapter ids).
+ */
+
+/*
+ * lora_segments_build over the choices expert_ids [T k] int32 (expert in [0,
+ * num_experts), or -1 for none), and pos [T k] int32: the place of every choice in
+ * the sorted order, -1 for a choice without an expert (or with a bad id, which *err
+ * counts).  seg and ws as for lora_segments_build of T k rows; k >= 1, T k <= 2^31 - 1.
+ */
+int lora_expert_segments(const int32_t* expert_ids, int32_t T, int32_t k, int32_t num_experts, lora_segments seg, int32_t* pos,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rows to their experts: y[pos[t k + j]] = x[t] for every choice with a place.
+ *   x [T, ldx], y [T k, ldy] (dtype), d columns; pos of lora_expert_segments (values
+ *   outside [0, T k) count as none).  Rows of y that no choice names are left as
+ *   they are.  One kernel; d a multiple of 8.
+ */
+int lora_expert_gather(int dtype, const void* x, int64_t ldx, int32_t T, int32_t d, int32_t k, const int32_t* pos, void* y, int64_t ldy,
+                       void* stream);
+
+/*
+ * Its gradient: dx[t] (+)= sum_j dy[pos[t k + j]], in the order of j, in fp32, rounded
+ * once (accumulate = 1 adds dx[t] last; accumulate = 0 writes zeros for a token
+ * without a choice).  dy [T k, lddy], dx [T, lddx] (dtype).  One kernel.
+ */
+int lora_expert_gather_backward(int dtype, const void* dy, int64_t lddy, int32_t T, int32_t d, int32_t k, const int32_t* pos, void* dx,
+                                int64_t lddx, int32_t accumulate, void* stream);
+
+/*
+ * Rows back from their experts: y[t] (+)= sum_j w[t k + j] o[pos[t k + j]], in the
+ * order of j, in fp32, rounded once (accumulate as above, e.g. onto a residual).
+ *   o [T k, ldo], y [T, ldy] (dtype); w [T k] fp32, the router's weights.  Choices
+ *   without a place add nothing, whatever their weight.  One kernel.
+ */
+int lora_expert_combine(int dtype, const void* o, int64_t ldo, int32_t T, int32_t d, int32_t k, const int32_t* pos, const float* w,
+                        void* y, int64_t ldy, int32_t accumulate, void* stream);
+
+/*
+ * Its gradient: d_o[pos[t k + j]] = w[t k + j] dy[t] (rounded once) and dw[t k + j] =
+ * sum over d of dy[t] o[pos[t k + j]] (fp32, a fixed order; 0 for a choice without a
+ * place).  dy [T, lddy], o [T k, ldo], d_o [T k, lddo] (dtype); dw [T k] fp32.  Rows
+ * of d_o that no choice names are left as they are; d_o may be NULL, and dw may be
+ * (then o is not read and may be too).  d_o may be o itself: a row is read before it
+ * is written.  One kernel.
+ */
+int lora_expert_combine_backward(int dtype, const void* dy, int64_t lddy, const void* o, int64_t ldo, int32_t T, int32_t d, int32_t k,
+                                 const int32_t* pos, const float* w, void* d_o, int64_t lddo, float* dw, void* stream);
+
+/*
+ * The experts' products: y_i (+)= W_e x_i for every sorted row i of expert e, in one
+ * launch, without a workspace and without the rows' numbers on the host.
+ *   x, x_bits, y, accumulate and what is summed: as for lora_base_product_mx, T sorted
+ *   rows (T k of the segments); w: the mx forms [num_experts d_out, d_in], expert e's
+ *   rows e d_out .. e d_out + d_out - 1 (dX: the transposed weights, one below the
+ *   other).  seg: of the choices (its offsets are read; num_experts as built).
+ * Rows from offsets[num_experts] on are neither read nor written.  Which kernel runs
+ * goes by the mean number of rows of an expert, so results are bit-reproducible for
+ * equal T, shapes and choices.
+ */
+int lora_expert_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t num_experts,
+                           int32_t d_out, lora_segments seg, void* y, int64_t ldy, int32_t accumulate, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
