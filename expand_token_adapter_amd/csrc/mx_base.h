@@ -62,51 +62,54 @@ struct MxGroup {
     int first, rows;  // of the tile
     int expert;
 };
-// Tiles of this lane's expert e, and where its rows begin and end.
-template <int BT>
-__device__ __forceinline__ int mx_tiles_of(const MxParams& p, int e, int& begin, int& end) {
-    begin = end = 0;
-    if (e < p.experts) {
-        begin = min(max(gptr(p.offsets)[e], 0), p.T);
-        end = min(max(gptr(p.offsets)[e + 1], begin), p.T);
-    }
-    return (end - begin + BT - 1) / BT;
-}
-__device__ __forceinline__ int mx_scan(int v, int lane) {
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int o = __shfl_up(v, d, kWave);
-        if (lane >= d) v += o;
-    }
-    return v;
+// Inclusive sum over the wave's lanes (in registers: 1, 2, 4, 8 lanes up within 16, then
+// the sums of 16 and of 32 lanes to those behind them).
+__device__ __forceinline__ int mx_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);
+    return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
 }
 template <int BT>
-__device__ __forceinline__ int mx_total_tiles(const MxParams& p, int lane) {
-    int total = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += kWave) {
-        int b, e;
-        total += __builtin_amdgcn_readlane(mx_scan(mx_tiles_of<BT>(p, e0 + lane, b, e), lane), kWave - 1);
+struct MxExperts {
+    int begin, end, incl;  // of this lane's expert: its rows, the tiles of the experts up to it
+    __device__ __forceinline__ static MxExperts load(const MxParams& p, int e) {
+        MxExperts x{0, 0, 0};
+        if (e < p.experts) {
+            x.begin = min(max(gptr(p.offsets)[e], 0), p.T);
+            x.end = min(max(gptr(p.offsets)[e + 1], x.begin), p.T);
+        }
+        x.incl = mx_scan(x.tiles());
+        return x;
     }
+    __device__ __forceinline__ int tiles() const { return (end - begin + BT - 1) / BT; }
+    __device__ __forceinline__ int total() const { return __builtin_amdgcn_readlane(incl, kWave - 1); }
+};
+// The number of tiles; first: experts 0 .. 63.
+template <int BT>
+__device__ __forceinline__ int mx_total_tiles(const MxParams& p, int lane, const MxExperts<BT>& first) {
+    int total = first.total();
+    for (int e0 = kWave; e0 < p.experts; e0 += kWave) total += MxExperts<BT>::load(p, e0 + lane).total();
     return total;
 }
 // (tile below the total)
 template <int BT>
-__device__ __forceinline__ MxGroup mx_find_tile(const MxParams& p, int tile, int lane) {
-    int before = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += kWave) {
-        int b, e;
-        const int n = mx_tiles_of<BT>(p, e0 + lane, b, e);
-        const int incl = mx_scan(n, lane);
-        const uint64_t past = __ballot(before + incl > tile);
+__device__ __forceinline__ MxGroup mx_find_tile(const MxParams& p, int tile, int lane, MxExperts<BT> x) {
+    for (int e0 = 0;;) {
+        const uint64_t past = __ballot(x.incl > tile);
         if (past) {
             const int at = __ffsll((long long)past) - 1;
-            const int in = tile - before - __builtin_amdgcn_readlane(incl - n, at);
-            const int begin = __builtin_amdgcn_readlane(b, at) + in * BT;
-            return MxGroup{begin, min(BT, __builtin_amdgcn_readlane(e, at) - begin), e0 + at};
+            const int in = tile - __builtin_amdgcn_readlane(x.incl - x.tiles(), at);
+            const int begin = __builtin_amdgcn_readlane(x.begin, at) + in * BT;
+            return MxGroup{begin, min(BT, __builtin_amdgcn_readlane(x.end, at) - begin), e0 + at};
         }
-        before += __builtin_amdgcn_readlane(incl, kWave - 1);
+        tile -= x.total();
+        e0 += kWave;
+        if (e0 >= p.experts) return MxGroup{0, 0, 0};
+        x = MxExperts<BT>::load(p, e0 + lane);
     }
-    return MxGroup{0, 0, 0};
 }
 
 // ------------------------------------------------------------------ operands
@@ -124,10 +127,10 @@ __device__ __forceinline__ i32x8_t mx_operand(u32x4_t q) { return i32x8_t{(int)q
 // A workgroup of WN x WT waves computes BN outputs x BT rows.  A step is 256 columns
 // of 4-bit rows or 128 of 8-bit rows, 128 bytes of an activation row; BN weight and
 // BT activation rows' steps go from memory straight into LDS, ST stages in a ring,
-// the step's scales into a ring of ST + 1.  The pieces of a step are handed over as
+// the scales a span of steps at a time (MxLds).  The pieces of a step are handed over as
 // in base.h: the weight blocks are taken two or four at a time, and after the barrier at the
 // start of such a group its place is free for the step ST later, whose loads go out
-// between the products.  Scales go out first: their slot was last read a step ago.
+// between the products.
 //
 // 16-byte unit c of a row lies at position c ^ s of it: s is the operand row modulo 8
 // for rows of 128 bytes, half of it modulo 4 for rows of 64 bytes, so that 8 lanes
@@ -145,7 +148,7 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     // loads of a wave: for a weight group, for the activations, for the scales
     constexpr int GR = GA * 16 * WN;                     // weight rows of a group
     constexpr int WU = GR / RW >= NW ? GR / RW / NW : 1, XU = BT / RX / NW;
-    constexpr int SU = (L::kChunksW + L::kChunksX + NW - 1) / NW;
+    constexpr int SU = (L::kLoadsW + L::kLoadsX + NW - 1) / NW;
     constexpr int PW = SU + NG * WU + XU;
     static_assert(FN % 2 == 0 && NG <= 4 && BT % (RX * NW) == 0, "the loads divide evenly");
     static_assert(GR / RW >= NW ? GR % (RW * NW) == 0 : NW % (GR / RW) == 0, "the weight's loads divide evenly");
@@ -156,20 +159,28 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     const int lane = threadIdx.x & (kWave - 1);
     const int lr = lane & 15, lg = lane >> 4;
     // Workgroups of one XCD take neighbouring tiles.
-    const int tiles_t = p.offsets ? mx_total_tiles<BT>(p, lane) : p.tiles_t;
+    MxExperts<BT> ex{0, 0, 0};
+    int tiles_t = p.tiles_t;
+    if (p.offsets) {
+        ex = MxExperts<BT>::load(p, lane);
+        tiles_t = mx_total_tiles<BT>(p, lane, ex);
+    }
     const int ntile = p.tiles_n * tiles_t * p.splits;
     const int per = (ntile + kNumXcd - 1) / kNumXcd;
     const int task = (int)(blockIdx.x % kNumXcd) * per + (int)(blockIdx.x / kNumXcd);
     if ((int)(blockIdx.x / kNumXcd) >= per || task >= ntile) return;
-    const int tile = task / p.splits, part = task - tile * p.splits;
-    const int k0 = (int)((int64_t)p.steps * part / p.splits), k1 = (int)((int64_t)p.steps * (part + 1) / p.splits);
+    const int tile = task / p.splits, kpart = task - tile * p.splits;
+    // this workgroup's steps: whole spans of scales
+    const int spans = (p.steps + L::kSpan - 1) / L::kSpan;
+    const int k0 = L::kSpan * (int)((int64_t)spans * kpart / p.splits);
+    const int k1 = min(p.steps, L::kSpan * (int)((int64_t)spans * (kpart + 1) / p.splits));
     // Order of the tiles: bands of up to kBand tiles along t, walked along n (base.h).
     const int band = tile / (kBand * p.tiles_n), in = tile - band * kBand * p.tiles_n;
     const int bt = min(kBand, tiles_t - band * kBand);
     const int n0 = in / bt * BN, tt = band * kBand + in % bt;
     MxGroup grp{tt * BT, 0, 0};
     if (p.offsets)
-        grp = mx_find_tile<BT>(p, tt, lane);
+        grp = mx_find_tile<BT>(p, tt, lane, ex);
     else
         grp.rows = min(BT, p.T - grp.first);
     const int t0 = grp.first, trows = grp.rows, nrows = min(BN, p.N - n0);
@@ -180,59 +191,100 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     const int64_t wrow = (int64_t)grp.expert * p.N + n0;
     const buf_rsrc_t rw = make_rsrc(p.w + wrow * p.ldw, (uint32_t)((nrows - 1) * p.ldw + (int64_t)p.steps * L::kRowW));
     const buf_rsrc_t rx = make_rsrc(p.x + (int64_t)t0 * p.ldx, (uint32_t)((trows - 1) * p.ldx + (int64_t)p.steps * L::kRowX));
-    const buf_rsrc_t rws = make_rsrc(p.ws + wrow * p.ldws, (uint32_t)((nrows - 1) * p.ldws + (int64_t)p.steps * L::kWordsW * 4));
-    const buf_rsrc_t rxs = make_rsrc(p.xs + (int64_t)t0 * p.ldxs,
-                                     (uint32_t)((trows - 1) * p.ldxs + (XB == 4 ? (int64_t)p.steps * 8 : (p.steps + 3) / 4 * 4)));
-    // Load j of weight group g: row group (RW rows) c of the group's GR rows, in the
-    // order wave column, row: rows 16 GA g .. 16 GA (g + 1) - 1 of every wave column.
-    constexpr int LWR = 64 / RW;  // lanes of a weight row's step
+    // The loads of a step, with what of their addresses stays the same (a row goes into the
+    // part of the address that is checked, the column into the other).
+    // Weights: load j of group g is RW rows, in the order wave column, row (rows 16 GA g ..
+    // 16 GA (g + 1) - 1 of every wave column); a wave without one repeats another's.
+    constexpr int CPG = 16 * GA / RW;  // loads of a wave column's group
+    constexpr int LWR = 64 / RW;       // lanes of a weight row's step
     const int wr = lane / LWR;
-    const int w_key = L::kRowW == 128 ? (wr & 3) : 2 * ((wr >> 3) & 1) + ((wr >> 1) & 1);
-    const int x_r8 = lane >> 3;
-    const uint32_t vx = (uint32_t)((8 * wave + x_r8) * p.ldx) + (uint32_t)((lane & 7) ^ x_r8) * 16u;
-    auto issue_w = [&](int g, int j, int slot, int kb) {
-        constexpr int CPG = 16 * GA / RW;                  // loads of a wave column's group
-        const int c = (wave + NW * j) % (CPG * WN);        // (a wave without one repeats another's)
-        const int row = c / CPG * (BN / WN) + 16 * GA * g + c % CPG * RW;
-        // (rows of 128 bytes: a load is 8 rows, and the next 8 have the other half of the keys)
-        const int key = L::kRowW == 128 ? w_key ^ ((c & 1) * 4) : w_key;
-        const uint32_t v = (uint32_t)((row + wr) * p.ldw) + (uint32_t)((lane % LWR) ^ key) * 16u;
-        dma_lds(rw, v, (uint32_t)kb * L::kRowW, s_lds + slot * L::kStage + row * L::kRowW, 16);
-    };
-    auto issue_x = [&](int j, int slot, int kb) {
-        dma_lds(rx, vx + (uint32_t)(8 * NW * j * p.ldx), (uint32_t)kb * L::kRowX,
-                s_lds + slot * L::kStage + BN * L::kRowW + (8 * wave + 8 * NW * j) * L::kRowX, 16);
-    };
-    auto issue_s = [&](int j, int sslot, int kb) {
-        const int c = (wave + NW * j) % (L::kChunksW + L::kChunksX);
-        char* at = s_sc + sslot * L::kScales + c * 256;
-        if (c < L::kChunksW) {
-            const int word = 64 * c + lane;
-            dma_lds(rws, (uint32_t)((word / L::kWordsW) * p.ldws) + (uint32_t)(word % L::kWordsW) * 4u,
-                    (uint32_t)kb * (L::kWordsW * 4), at, 4);
-        } else {
-            const int word = 64 * (c - L::kChunksW) + lane;
-            dma_lds(rxs, (uint32_t)((word / L::kWordsX) * p.ldxs) + (uint32_t)(word % L::kWordsX) * 4u,
-                    XB == 4 ? (uint32_t)kb * 8u : (uint32_t)kb & ~3u, at, 4);
+    // (rows of 128 bytes: a load is 8 rows, and the next 8 have the other half of the keys)
+    const int w_key = L::kRowW == 128 ? (wr & 3) ^ ((wave & 1) * 4) : 2 * ((wr >> 3) & 1) + ((wr >> 1) & 1);
+    static_assert(CPG * WN % 2 == 0 && NW % 2 == 0, "a wave's loads have one parity");
+    uint32_t vw[NG][WU], vx[XU];
+    int lds_w[NG][WU], lds_x[XU];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int j = 0; j < WU; ++j) {
+            const int c = (wave + NW * j) % (CPG * WN);
+            const int row = c / CPG * (BN / WN) + 16 * GA * g + c % CPG * RW;
+            vw[g][j] = (uint32_t)((row + wr) * p.ldw) + (uint32_t)((lane % LWR) ^ w_key) * 16u;
+            lds_w[g][j] = row * L::kRowW;
         }
+#pragma unroll
+    for (int j = 0; j < XU; ++j) {
+        const int row = 8 * (wave + NW * j);
+        vx[j] = (uint32_t)((row + (lane >> 3)) * p.ldx) + (uint32_t)((lane & 7) ^ (lane >> 3)) * 16u;
+        lds_x[j] = BN * L::kRowW + row * L::kRowX;
+    }
+    // Scales: load j of this wave is 64 words of weight or of activation rows; those that go
+    // out for place q of a span are of the next span, their part q of its rows.  8 words of
+    // a row are exchanged by the row (4: by half as much), so that the rows that a read takes
+    // together fall on different banks.
+    constexpr int kKeyW = L::kWordsW == 8 ? 3 : 1, kKeyX = L::kWordsX == 8 ? 1 : 0;
+    uint32_t vs[SU][L::kSpan];
+    int lds_s[SU][L::kSpan], s_step[SU], s_left[SU];
+    const uint8_t* s_base[SU];
+#pragma unroll
+    for (int j = 0; j < SU; ++j) {
+        const int c = (wave + NW * j) % (L::kLoadsW + L::kLoadsX);
+        const bool of_w = c < L::kLoadsW;
+        const int words = of_w ? L::kWordsW : L::kWordsX;
+        const uint32_t ld = (uint32_t)(of_w ? p.ldws : p.ldxs);
+        s_step[j] = words * 4;
+        s_base[j] = (of_w ? p.ws + wrow * p.ldws : p.xs + (int64_t)t0 * p.ldxs) + k0 / L::kSpan * s_step[j];
+        s_left[j] = (int)(of_w ? (nrows - 1) * p.ldws + (int64_t)p.steps * (L::kRowW / 16)
+                               : (trows - 1) * p.ldxs + (XB == 4 ? (int64_t)p.steps * 8 : (p.steps + 3) / 4 * 4)) -
+                    k0 / L::kSpan * s_step[j];
+#pragma unroll
+        for (int q = 0; q < L::kSpan; ++q) {
+            const int m = of_w ? (q * L::kLoadsW + c) % L::kAllW : (q * L::kLoadsX + c - L::kLoadsW) % L::kAllX;
+            vs[j][q] = (uint32_t)(m * (64 / words) + lane / words) * ld +
+                       ((uint32_t)(lane % words) * 4u ^ (uint32_t)((m & (of_w ? kKeyW : kKeyX)) * 8));
+            lds_s[j][q] = (of_w ? 0 : L::kAllW * 256) + m * 256;
+        }
+    }
+    buf_rsrc_t rs[SU];
+    auto span_rsrc = [&]() {
+#pragma unroll
+        for (int j = 0; j < SU; ++j) rs[j] = make_rsrc(s_base[j], (uint32_t)max(s_left[j], 0));
+    };
+    auto next_span = [&]() {  // the scales' loads that follow are of the next span
+#pragma unroll
+        for (int j = 0; j < SU; ++j) {
+            s_base[j] += s_step[j];
+            s_left[j] -= s_step[j];
+        }
+        span_rsrc();
     };
     // Load o of a step: scales, weight group 0, activations, weight groups 1, 2, ...
-    auto issue = [&](int o, int slot, int sslot, int kb) {
+    // slot, kb: the step's place in the ring and along k; q, to: its place in the span, and
+    // where the scales go
+    auto issue = [&](int o, int slot, int kb, int q, int to) {
+        char* at = s_lds + slot * L::kStage;
         if (o < SU)
-            issue_s(o, sslot, kb);
+            dma_lds(rs[o], vs[o][q], 0u, s_sc + to + lds_s[o][q], 4);
         else if (o < SU + WU)
-            issue_w(0, o - SU, slot, kb);
+            dma_lds(rw, vw[0][o - SU], (uint32_t)kb * L::kRowW, at + lds_w[0][o - SU], 16);
         else if (o < SU + WU + XU)
-            issue_x(o - SU - WU, slot, kb);
+            dma_lds(rx, vx[o - SU - WU], (uint32_t)kb * L::kRowX, at + lds_x[o - SU - WU], 16);
         else
-            issue_w((o - SU - XU) / WU, (o - SU - XU) % WU, slot, kb);
+            dma_lds(rw, vw[(o - SU - XU) / WU][(o - SU - XU) % WU], (uint32_t)kb * L::kRowW,
+                    at + lds_w[(o - SU - XU) / WU][(o - SU - XU) % WU], 16);
     };
 
+    // (Zeros that the compiler does not see as one constant: with that it copies every sum
+    // to the loop's registers and back in each step: 2048 x 4096 x 4096 from 8-bit rows,
+    // 256 x 128 tiles, 44.6 us in place of 30.)
     f32x4_t acc[FN][FT];
 #pragma unroll
     for (int a = 0; a < FN; ++a)
 #pragma unroll
-        for (int b = 0; b < FT; ++b) acc[a][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < FT; ++b) {
+            acc[a][b] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            asm volatile("" : "+v"(acc[a][b]));
+        }
 
     // This lane's units of an operand row.  Weight row of operand row lr: 8 (lr / 4) +
     // lr % 4 of the pair of blocks, + 4 for its second block.
@@ -242,28 +294,33 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     const int lrow_x = lr * L::kRowX + (((kDecode ? 2 * lg : lg) ^ (lr & 7)) * 16);
     constexpr int kOther = kDecode ? 16 : 64;
     u32x4_t a[2][GA][SUB], b[FT][2];
-    uint32_t wsc[2][GA][SUB], xsc[FT][L::kWordsX];
+    constexpr int SX = XB == 4 ? 2 : 1;
+    uint32_t wsc[2][GA][SUB], xsc[FT][SX];
     auto read_a = [&](int buf, int f, int u, int slot, int g) {
         const int blk = GA * g + f;
         const char* at = s_lds + slot * L::kStage + (wn + 32 * (blk / 2) + 4 * (blk & 1)) * L::kRowW;
         a[buf][f][u] = *reinterpret_cast<const u32x4_t*>(at + (u ? lrow_w ^ 64 : lrow_w));
     };
-    auto read_ws = [&](int buf, int f, int sslot, int g) {
+    // scales of a step: its place in the span, exchanged as the row's words are
+    constexpr int kPartW = L::kRowW / 16;  // bytes of a weight row's step
+    const int srow_w = (8 * (lr >> 2) + (lr & 3)) * L::kWordsW * 4 + (L::kWordsW == 8 ? lr >> 2 : lr >> 3) * 8;
+    const int srow_x = L::kAllW * 256 + lr * L::kWordsX * 4 + (L::kWordsX == 8 ? (lr >> 3) * 8 : 0);
+    auto read_ws = [&](int buf, int f, const char* at, int part, int g) {
         const int blk = GA * g + f;
-        const int row = wn + 32 * (blk / 2) + 4 * (blk & 1) + 8 * (lr >> 2) + (lr & 3);
-        const uint32_t* at = reinterpret_cast<const uint32_t*>(s_sc + sslot * L::kScales) + row * L::kWordsW;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(at + (wn + 32 * (blk / 2) + 4 * (blk & 1)) * L::kWordsW * 4 +
+                                                              (srow_w ^ (part * kPartW)));
 #pragma unroll
-        for (int u = 0; u < SUB; ++u) wsc[buf][f][u] = at[u];
+        for (int u = 0; u < SUB; ++u) wsc[buf][f][u] = w[u];
     };
     auto read_b = [&](int h, int u, int slot) {
         b[h][u] = *reinterpret_cast<const u32x4_t*>(s_lds + slot * L::kStage + BN * L::kRowW + (wt + 16 * h) * L::kRowX +
                                                     (u ? lrow_x ^ kOther : lrow_x));
     };
-    auto read_xs = [&](int h, int sslot) {
-        const uint32_t* at =
-            reinterpret_cast<const uint32_t*>(s_sc + sslot * L::kScales + L::kChunksW * 256) + (wt + 16 * h + lr) * L::kWordsX;
+    auto read_xs = [&](int h, const char* at, int part) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(at + (wt + 16 * h) * L::kWordsX * 4 +
+                                                              (XB == 4 ? srow_x ^ (part * 8) : srow_x + (part >> 2) * 4));
 #pragma unroll
-        for (int u = 0; u < L::kWordsX; ++u) xsc[h][u] = at[u];
+        for (int u = 0; u < SX; ++u) xsc[h][u] = w[u];
     };
     // The byte of lane group lg of the words of a step's 128-column parts, in bytes 0 and 1.
     const uint32_t sel = 0x0c0c0400u + (uint32_t)lg * 0x0101u;
@@ -275,33 +332,52 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     };
 
     const int nk = k1 - k0;
+    // the first span's scales, then the first steps (and with them the second span's)
+    span_rsrc();
+#pragma unroll
+    for (int q = 0; q < L::kSpan; ++q)
+#pragma unroll
+        for (int o = 0; o < SU; ++o) issue(o, 0, 0, q, 0);
+    next_span();
 #pragma unroll
     for (int s = 0; s < ST; ++s)
 #pragma unroll
-        for (int o = 0; o < PW; ++o) issue(o, s, s, k0 + min(s, nk - 1));
+        for (int o = 0; o < PW; ++o) issue(o, s, k0 + min(s, nk - 1), s % L::kSpan, L::kScales);
     wait_vmcnt_le<PW*(ST - 1)>();
     lds_barrier();
 #pragma unroll
     for (int f = 0; f < GA; ++f) {
 #pragma unroll
         for (int u = 0; u < SUB; ++u) read_a(0, f, u, 0, 0);
-        read_ws(0, f, 0, 0);
+        read_ws(0, f, s_sc, 0, 0);
     }
 #pragma unroll
     for (int h = 0; h < FT; ++h) {
         read_b(h, 0, 0);
         read_b(h, 1, 0);
-        read_xs(h, 0);
+        read_xs(h, s_sc, 0);
     }
-    int slot = 0, sslot = 0;
-    constexpr auto before = [](int g) { return PW * g / NG; };  // loads of a step that go out before its group g
+    // loads of a step that go out before its group g
+    constexpr auto before = [](int g) { return PW * g / NG; };
     static_assert(before(1) <= SU + WU + XU, "a group's place is free when its loads go out");
-    auto step = [&](auto parity, int i) {
-        constexpr int P = decltype(parity)::value;  // (an odd number of groups: the buffers of a change places each step)
-        const int next = slot + 1 == ST ? 0 : slot + 1;
-        const int snext = sslot + 1 == ST + 1 ? 0 : sslot + 1;
-        const int sold = sslot == 0 ? ST : sslot - 1;  // the slot of the step before, for the step ST later
+    // where the scales lie of the span that is read, and those are loaded that go out now
+    int read_at = 0, load_at = L::kScales;
+    auto after_slot = [](int at) { return at == (L::kSlots - 1) * L::kScales ? 0 : at + L::kScales; };
+    // Step i, place q modulo its span's steps: places in the rings are known when the code is made (half
+    // of a step's instructions were their arithmetic, and a wave alone on its SIMD takes a
+    // few cycles for each: 256 x 4096 x 4096 from 8-bit rows XXX).
+    auto step = [&](auto place, int i) {
+        constexpr int q = decltype(place)::value, slot = q % ST, next = (q + 1) % ST;
+        constexpr int part = q % L::kSpan, npart = (q + 1) % L::kSpan, lpart = (q + ST) % L::kSpan;
+        constexpr int P = q & 1;  // (an odd number of groups: the buffers of a change places each step)
         const int kn = k0 + min(i + ST, nk - 1);
+        if constexpr (lpart == 0) {
+            next_span();
+            load_at = after_slot(load_at);
+        }
+        const char* sc = s_sc + read_at;
+        if constexpr (npart == 0) read_at = after_slot(read_at);
+        const char* nsc = s_sc + read_at;
         auto group = [&](auto gc) {
             constexpr int g = decltype(gc)::value;
             constexpr bool last = g + 1 == NG;
@@ -339,7 +415,7 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
                                                                              1, (int)as[f], 1, (int)bs);
                     }
                 } else {
-                    const uint32_t bs = xsc[h][0] >> (8 * ((k0 + min(i, nk - 1)) & 3));
+                    const uint32_t bs = xsc[h][0] >> (8 * (part & 3));
                     if constexpr (kDecode) {
                         const float s = quant_scale(bs & 255u);
                         const Frag<LORA_BF16> bq[4] = {dequant8<LORA_BF16>(b[h][0][0], b[h][0][1], s),
@@ -370,16 +446,16 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
                     if (u < SUB)
                         read_a(nxt, f, u, last ? next : slot, last ? 0 : g + 1);
                     else
-                        read_ws(nxt, f, last ? snext : sslot, last ? 0 : g + 1);
+                        read_ws(nxt, f, last ? nsc : sc, last ? npart : part, last ? 0 : g + 1);
                 }
                 if (last) {
                     read_b(h, 0, next);
                     read_b(h, 1, next);
-                    read_xs(h, snext);
+                    read_xs(h, nsc, npart);
                 }
                 constexpr int o0 = before(g), n = before(g + 1) - o0;
 #pragma unroll
-                for (int o = o0 + h * n / FT; o < o0 + (h + 1) * n / FT; ++o) issue(o, slot, sold, kn);
+                for (int o = o0 + h * n / FT; o < o0 + (h + 1) * n / FT; ++o) issue(o, slot, kn, lpart, load_at);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -387,12 +463,20 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
         if constexpr (NG > 1) group(std::integral_constant<int, 1 % NG>{});
         if constexpr (NG > 2) group(std::integral_constant<int, 2 % NG>{});
         if constexpr (NG > 3) group(std::integral_constant<int, 3 % NG>{});
-        slot = next;
-        sslot = snext;
     };
-    for (int i = 0; i < nk; i += 2) {
+    constexpr int U = L::kSpan < 4 ? 4 : L::kSpan;
+    static_assert(U <= 8 && U % L::kSpan == 0 && U % ST == 0, "a span's steps take whole rounds of the ring");
+    for (int i = 0; i < nk; i += U) {
         step(std::integral_constant<int, 0>{}, i);
-        if (i + 1 < nk) step(std::integral_constant<int, NG & 1>{}, i + 1);
+        if (i + 1 < nk) step(std::integral_constant<int, 1>{}, i + 1);
+        if (i + 2 < nk) step(std::integral_constant<int, 2>{}, i + 2);
+        if (i + 3 < nk) step(std::integral_constant<int, 3>{}, i + 3);
+        if constexpr (U > 4) {
+            if (i + 4 < nk) step(std::integral_constant<int, 4 % U>{}, i + 4);
+            if (i + 5 < nk) step(std::integral_constant<int, 5 % U>{}, i + 5);
+            if (i + 6 < nk) step(std::integral_constant<int, 6 % U>{}, i + 6);
+            if (i + 7 < nk) step(std::integral_constant<int, 7 % U>{}, i + 7);
+        }
     }
     wait_vmcnt_le<0>();  // nothing may land in LDS after the workgroup has ended
 #pragma unroll
@@ -401,7 +485,7 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
         const bool t_in = tl < trows;
         const int64_t t = t0 + (t_in ? tl : 0);
         if (p.splits > 1) {
-            float* row = p.part + ((int64_t)part * p.T + t) * p.N;
+            float* row = p.part + ((int64_t)kpart * p.T + t) * p.N;
 #pragma unroll
             for (int f = 0; f < FN; f += 2) {
                 const int n = n0 + wn + 16 * f + 8 * lg;
@@ -435,107 +519,180 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     }
 }
 
-// ------------------------------------------------------------------ few rows: the weight as a stream
+// ------------------------------------------------------------------ few rows: waves side by side along k
 //
-// Up to 16 rows a tile: the weight is read straight into operand registers and nothing
-// of it is shared between waves.  A workgroup of NW waves computes 16 outputs of a
-// tile's rows; wave w takes the steps w, w + NW, ... of 256 columns (128 bytes of a
-// weight row), kMxU of them in flight, and the waves' sums are added in wave order
-// through LDS.
-constexpr int kMxU = 2;
-
-template <int NW, int XB, int DT>
+// A workgroup of NW waves computes 16 FN outputs x 16 FT rows; wave w takes the pieces
+// w, w + NW, ... of 512 columns (256 bytes of a weight row, 16 of its scales) for the whole
+// tile, so no byte of the operands is wanted by two of its waves: they go from memory
+// straight into operand registers, a piece ahead, without LDS and without a barrier until
+// the waves' sums are added, in wave order, through LDS.  Rows that do not exist and
+// columns past the end lie past their buffer: nothing is fetched for them.
+template <int NW, int FN, int FT, int XB, int DT>
 __global__ __launch_bounds__(NW* kWave) void mx_stream_kernel(MxParams p) {
     constexpr bool kDecode = kMxDecode<XB, DT>;
-    __shared__ f32x4_t s_acc[NW][kWave];
+    constexpr int XH = XB == 4 ? 1 : 2;  // 16-byte units of a lane for 128 columns of an activation row
+    __shared__ f32x4_t s_acc[NW][FN * FT][kWave];
     const int wave = wave_id();
     const int lane = threadIdx.x & (kWave - 1);
     const int lr = lane & 15, lg = lane >> 4;
-    int n0 = blockIdx.x * 16;
-    MxGroup grp{0, p.T, 0};
+    // Workgroups of one XCD take neighbouring tiles: of one weight block's rows, or of one
+    // expert's tile of rows.
+    MxExperts<16 * FT> ex{0, 0, 0};
+    int tiles_t = p.tiles_t;
     if (p.offsets) {
-        const int tiles = mx_total_tiles<16>(p, lane);
-        const int tile = blockIdx.x / p.tiles_n;
-        if (tile >= tiles) return;
-        n0 = (blockIdx.x - tile * p.tiles_n) * 16;
-        grp = mx_find_tile<16>(p, tile, lane);
+        ex = MxExperts<16 * FT>::load(p, lane);
+        tiles_t = mx_total_tiles<16 * FT>(p, lane, ex);
     }
-    const int64_t wrow = (int64_t)grp.expert * p.N + min(n0 + lr, p.N - 1);
-    const LORA_GLOBAL uint8_t* w = gptr(p.w + wrow * p.ldw + 16 * lg);
-    const LORA_GLOBAL uint8_t* ws = gptr(p.ws + wrow * p.ldws);
-    const int64_t row = grp.first + min(lr, grp.rows - 1);
-    const LORA_GLOBAL uint8_t* x = gptr(p.x + row * p.ldx + (kDecode ? 32 : 16) * lg);
-    const LORA_GLOBAL uint8_t* xs = gptr(p.xs + row * p.ldxs);
-    const uint32_t sel = 0x0c0c0400u + (uint32_t)lg * 0x0101u;
-    f32x4_t acc{0.f, 0.f, 0.f, 0.f};
-    // p.steps: of 128 columns for 8-bit rows (an odd number leaves the last step's second
-    // half without a column), of 256 for 4-bit rows
-    const int steps = XB == 4 ? p.steps : (p.steps + 1) / 2;
-    for (int k0 = wave; k0 < steps; k0 += NW * kMxU) {
-        u32x4_t a[kMxU][2], b[kMxU][XB == 4 ? 2 : 4];
-        u32x2_t as[kMxU], bs[kMxU];
+    const int ntile = p.tiles_n * tiles_t;
+    const int per = (ntile + kNumXcd - 1) / kNumXcd;
+    const int tile = (int)(blockIdx.x % kNumXcd) * per + (int)(blockIdx.x / kNumXcd);
+    if ((int)(blockIdx.x / kNumXcd) >= per || tile >= ntile) return;
+    int n0, tt;
+    if (p.offsets) {
+        tt = tile / p.tiles_n;
+        n0 = (tile - tt * p.tiles_n) * 16 * FN;
+    } else {
+        n0 = tile / tiles_t * 16 * FN;
+        tt = tile % tiles_t;
+    }
+    MxGroup grp{tt * 16 * FT, min(16 * FT, p.T - tt * 16 * FT), 0};
+    if (p.offsets) grp = mx_find_tile<16 * FT>(p, tt, lane, ex);
+    const int nrows = min(16 * FN, p.N - n0);
+    const int64_t wrow = (int64_t)grp.expert * p.N + n0;
+    const int blocks = XB == 4 ? 2 * p.steps : p.steps;  // of 128 columns
+    const int pieces = (blocks + 3) / 4;
+    const uint32_t bytes_w = (uint32_t)((nrows - 1) * p.ldw + (int64_t)blocks * 64);
+    const uint32_t bytes_ws = (uint32_t)((nrows - 1) * p.ldws + (int64_t)blocks * 4);
+    const uint32_t bytes_x = (uint32_t)((grp.rows - 1) * p.ldx + (int64_t)blocks * (XB * 16));
+    const uint32_t bytes_xs = (uint32_t)((grp.rows - 1) * p.ldxs + (XB == 4 ? (int64_t)blocks * 4 : (blocks + 3) / 4 * 4));
+    const uint8_t *w0 = p.w + wrow * p.ldw, *ws0 = p.ws + wrow * p.ldws;
+    const uint8_t *x0 = p.x + grp.first * p.ldx, *xs0 = p.xs + grp.first * p.ldxs;
+    uint32_t vw[FN], vws[FN], vx[FT], vxs[FT];
 #pragma unroll
-        for (int u = 0; u < kMxU; ++u) {
-            const int kb = min(k0 + NW * u, steps - 1);
+    for (int f = 0; f < FN; ++f) {
+        vw[f] = (uint32_t)((16 * f + lr) * p.ldw) + 16u * lg;
+        vws[f] = (uint32_t)((16 * f + lr) * p.ldws);
+    }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                a[u][i] = __builtin_nontemporal_load(reinterpret_cast<const LORA_GLOBAL u32x4_t*>(w + kb * 128 + 64 * i));
-            as[u] = *reinterpret_cast<const LORA_GLOBAL u32x2_t*>(ws + kb * 8);
-            if constexpr (XB == 4) {
+    for (int h = 0; h < FT; ++h) {
+        vx[h] = (uint32_t)((16 * h + lr) * p.ldx) + (kDecode ? 32u : 16u) * lg;
+        vxs[h] = (uint32_t)((16 * h + lr) * p.ldxs);
+    }
+    f32x4_t acc[FN][FT];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) b[u][i] = *reinterpret_cast<const LORA_GLOBAL u32x4_t*>(x + kb * 128 + 64 * i);
-                bs[u] = *reinterpret_cast<const LORA_GLOBAL u32x2_t*>(xs + kb * 8);
-            } else {
+    for (int f = 0; f < FN; ++f)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int kx = min(2 * kb + i, p.steps - 1);
+        for (int h = 0; h < FT; ++h) {
+            acc[f][h] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            asm volatile("" : "+v"(acc[f][h]));  // (as in mx_kernel)
+        }
+    struct Piece {
+        u32x4_t a[FN][4], b[FT][4 * XH];
+        u32x4_t as[FN], bs[FT];  // scales of the four blocks of 128 columns: words (8-bit rows: the bytes of a word)
+    };
+    // (a piece's columns come with the base, which is the same for all lanes, and the buffer
+    // ends where the last row's columns do)
+    auto load = [&](Piece& r, int k) {
+        const int64_t cw = (int64_t)k * 256, cx = (int64_t)k * (XB * 64), cs = (int64_t)k * 16, csx = XB == 4 ? cs : (int64_t)k * 4;
+        const buf_rsrc_t rw = make_rsrc(w0 + cw, bytes_w - (uint32_t)cw), rws = make_rsrc(ws0 + cs, bytes_ws - (uint32_t)cs);
+        const buf_rsrc_t rx = make_rsrc(x0 + cx, bytes_x - (uint32_t)cx), rxs = make_rsrc(xs0 + csx, bytes_xs - (uint32_t)csx);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        b[u][2 * i + h] = *reinterpret_cast<const LORA_GLOBAL u32x4_t*>(x + kx * 128 + (kDecode ? 16 : 64) * h);
-                    bs[u][i] = xs[kx];
-                }
-            }
+        for (int f = 0; f < FN; ++f) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.a[f][i] = buf_load16(rw, vw[f] + 64u * i, 0u);
+            r.as[f] = buf_load16(rws, vws[f], 0u);
         }
 #pragma unroll
-        for (int u = 0; u < kMxU; ++u) {
-            const int kb = k0 + NW * u;
-            if (kb >= steps) break;
-            const uint32_t sa = __builtin_amdgcn_perm(as[u][1], as[u][0], sel);
-            if constexpr (XB == 4) {
-                const uint32_t sb = __builtin_amdgcn_perm(bs[u][1], bs[u][0], sel);
-                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(a[u][0]), mx_operand(b[u][0]), acc, 4, 4, 0, (int)sa,
-                                                                       0, (int)sb);
-                acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(a[u][1]), mx_operand(b[u][1]), acc, 4, 4, 1, (int)sa,
-                                                                       1, (int)sb);
-            } else {
+        for (int h = 0; h < FT; ++h) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (2 * kb + i >= p.steps) break;
-                    if constexpr (kDecode) {
-                        const float fa = quant_scale((sa >> (8 * i)) & 255u), fb = quant_scale(bs[u][i]);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            acc = mma(mx_decode8<LORA_BF16>(a[u][i][c], fa),
-                                      dequant8<LORA_BF16>(b[u][2 * i + c / 2][2 * (c & 1)], b[u][2 * i + c / 2][2 * (c & 1) + 1], fb), acc);
-                    } else {
-                        const i32x8_t bo = __builtin_bit_cast(
-                            i32x8_t, __builtin_shufflevector(b[u][2 * i], b[u][2 * i + 1], 0, 1, 2, 3, 4, 5, 6, 7));
-                        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(a[u][i]), bo, acc, 4, 0, 0,
-                                                                               (int)(sa >> (8 * i)), 0, (int)bs[u][i]);
+                for (int u = 0; u < XH; ++u)
+                    r.b[h][XH * i + u] = buf_load16(rx, vx[h] + (uint32_t)(XB * 16 * i + (kDecode ? 16 : 64) * u), 0u);
+            if constexpr (XB == 4)
+                r.bs[h] = buf_load16(rxs, vxs[h], 0u);
+            else
+                r.bs[h][0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rxs, (int)vxs[h], 0, 0);
+        }
+    };
+    auto multiply = [&](const Piece& r, int k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (4 * k + i >= blocks) break;
+            uint32_t as[FN], bs[FT];
+#pragma unroll
+            for (int f = 0; f < FN; ++f) as[f] = r.as[f][i] >> (8 * lg);
+#pragma unroll
+            for (int h = 0; h < FT; ++h) bs[h] = XB == 4 ? r.bs[h][i] >> (8 * lg) : r.bs[h][0] >> (8 * i);
+            if constexpr (kDecode) {
+                Frag<LORA_BF16> bq[FT][4];
+#pragma unroll
+                for (int h = 0; h < FT; ++h) {
+                    const float s = quant_scale(bs[h] & 255u);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const u32x4_t q = r.b[h][XH * i + c / 2];
+                        bq[h][c] = dequant8<LORA_BF16>(q[2 * (c & 1)], q[2 * (c & 1) + 1], s);
                     }
                 }
+#pragma unroll
+                for (int f = 0; f < FN; ++f) {
+                    const float s = quant_scale(as[f] & 255u);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const Frag<LORA_BF16> aq = mx_decode8<LORA_BF16>(r.a[f][i][c], s);
+#pragma unroll
+                        for (int h = 0; h < FT; ++h) acc[f][h] = mma(aq, bq[h][c], acc[f][h]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int f = 0; f < FN; ++f)
+#pragma unroll
+                    for (int h = 0; h < FT; ++h) {
+                        if constexpr (XB == 4) {
+                            acc[f][h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                mx_operand(r.a[f][i]), mx_operand(r.b[h][i]), acc[f][h], 4, 4, 0, (int)as[f], 0, (int)bs[h]);
+                        } else {
+                            const i32x8_t bo = __builtin_bit_cast(
+                                i32x8_t, __builtin_shufflevector(r.b[h][XH * i], r.b[h][XH * i + XH - 1], 0, 1, 2, 3, 4, 5, 6, 7));
+                            acc[f][h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(r.a[f][i]), bo, acc[f][h], 4, 0, 0,
+                                                                                         (int)as[f], 0, (int)bs[h]);
+                        }
+                    }
             }
         }
+    };
+    Piece r0, r1;
+    if (wave < pieces) {
+        load(r0, wave);
+        for (int k = wave;; k += 2 * NW) {
+            if (k + NW >= pieces) {
+                multiply(r0, k);
+                break;
+            }
+            load(r1, k + NW);
+            multiply(r0, k);
+            if (k + 2 * NW >= pieces) {
+                multiply(r1, k + NW);
+                break;
+            }
+            load(r0, k + 2 * NW);
+            multiply(r1, k + NW);
+        }
     }
-    s_acc[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0) {
-        f32x4_t sum = s_acc[0][lane];
 #pragma unroll
-        for (int v = 1; v < NW; ++v) sum += s_acc[v][lane];
-        const int n = n0 + 4 * lg;
-        if (lr < grp.rows && n < p.N) {  // (N is a multiple of 8: the four are in or out together)
-            char* at = p.y + ((grp.first + lr) * p.ldy + n) * Frag<DT>::kBytes;
+    for (int f = 0; f < FN; ++f)
+#pragma unroll
+        for (int h = 0; h < FT; ++h) s_acc[wave][f * FT + h][lane] = acc[f][h];
+    __syncthreads();
+    for (int blk = wave; blk < FN * FT; blk += NW) {
+        f32x4_t sum = s_acc[0][blk][lane];
+#pragma unroll
+        for (int v = 1; v < NW; ++v) sum += s_acc[v][blk][lane];
+        const int n = n0 + 16 * (blk / FT) + 4 * lg, t = 16 * (blk % FT) + lr;
+        if (t < grp.rows && n < p.N) {  // (N is a multiple of 8: the four are in or out together)
+            char* at = p.y + ((grp.first + t) * p.ldy + n) * Frag<DT>::kBytes;
             if (p.accumulate) {
                 if constexpr (DT == LORA_BF16) {
                     const u32x2_t o = *gptr(reinterpret_cast<const u32x2_t*>(at));

@@ -14,32 +14,34 @@ namespace {
 template <int XB, int DT, int KIND, int WN, int WT>
 void launch_tiles(const MxParams& p, unsigned grid, hipStream_t st) {
     constexpr MxTile c = kMxTiles[KIND];
-    static_assert(WN * WT * kWave <= c.threads, "the plan's bound on the launch");
+    static_assert(WN * WT <= c.waves, "the plan's bound on the launch");
     hipLaunchKernelGGL((mx_kernel<c.bn, c.bt, WN, WT, XB == 4 ? c.stages4 : c.stages8, XB, DT>), dim3(grid), dim3(WN * WT * kWave), 0,
                        st, p);
+}
+template <int XB, int DT, int KIND>
+void launch_stream(const MxParams& p, unsigned grid, hipStream_t st) {
+    constexpr MxTile c = kMxTiles[KIND];
+    hipLaunchKernelGGL((mx_stream_kernel<c.waves, c.bn / 16, c.bt / 16, XB, DT>), dim3(grid),
+                       dim3(c.waves * kWave), 0, st, p);
 }
 
 // tiles_t: tiles along t of all weights, at most
 template <int XB, int DT>
 int launch_mx(MxParams p, const BasePlan& b, int64_t tiles_t, hipStream_t st) {
     p.splits = b.splits;
-    if (b.kind == kMxStream) {
-        p.tiles_n = (p.N + 15) / 16;
-        hipLaunchKernelGGL((mx_stream_kernel<kMxStreamWaves, XB, DT>), dim3((unsigned)(p.tiles_n * tiles_t)),
-                           dim3(kMxStreamWaves * kWave), 0, st, p);
-        return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
-    }
     const MxTile& c = kMxTiles[b.kind];
     p.tiles_n = (p.N + c.bn - 1) / c.bn;
     p.tiles_t = (int32_t)tiles_t;
     const unsigned grid = (unsigned)round_up(p.tiles_n * tiles_t * p.splits, kNumXcd);
     switch (b.kind) {
-        case kMx32x64: launch_tiles<XB, DT, kMx32x64, 1, 4>(p, grid, st); break;
         case kMx64x64: launch_tiles<XB, DT, kMx64x64, 2, 2>(p, grid, st); break;
-        case kMx64x128: launch_tiles<XB, DT, kMx64x128, 2, 2>(p, grid, st); break;
         case kMx128x128: launch_tiles<XB, DT, kMx128x128, 2, 2>(p, grid, st); break;
         case kMx256x128: launch_tiles<XB, DT, kMx256x128, 2, 2>(p, grid, st); break;
-        default: launch_tiles<XB, DT, kMx256x256, 2, 4>(p, grid, st); break;
+        case kMx256x256:
+            if constexpr (mx_kind_on(kMx256x256, XB, DT)) launch_tiles<XB, DT, kMx256x256, 2, 4>(p, grid, st);
+            break;
+        case kMx16x16: launch_stream<XB, DT, kMx16x16>(p, grid, st); break;
+        default: launch_stream<XB, DT, kMx32x16>(p, grid, st); break;
     }
     if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
     if (p.splits > 1) {
@@ -123,7 +125,7 @@ extern "C" int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int
     if (!ws || !aligned16(ws) || ws_bytes < base_workspace_bytes(b, T, d_out)) return LORA_ERR_WORKSPACE;
     MxParams p = product_params(x_bits, x, T, d_in, w, d_out, y, ldy, accumulate);
     p.part = static_cast<float*>(ws);
-    return launch(p, x_bits, dtype, b, b.kind == kMxStream ? 1 : (T + kMxTiles[b.kind].bt - 1) / kMxTiles[b.kind].bt, stream);
+    return launch(p, x_bits, dtype, b, (T + kMxTiles[b.kind].bt - 1) / kMxTiles[b.kind].bt, stream);
 }
 
 extern "C" int lora_expert_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t num_experts,

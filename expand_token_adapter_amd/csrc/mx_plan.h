@@ -1,5 +1,18 @@
 // mx_plan.h -- which kernel, tile and split of k a product with a 4-bit weight takes,
 // and the LDS of a tile (host and device, no HIP).
+//
+// Measured (us, bf16 y, 4-bit / 8-bit rows; rows x k x outputs; the last two kernels read
+// the weight straight into registers):
+//                          64x64      128x128    256x128    256x256    16x16      32x16
+//     1 x  4096 x  4096  6.5/8.0                                      3.4/3.7    4.6/4.8
+//    16 x 14336 x  4096   16/21                                       9.7/12.8    13/16
+//    32 x  4096 x  4096  6.8/8.6                                      6.7/8.7    5.7/6.8
+//   256 x  4096 x  4096  8.0/10.8    13/16      19/26      28/40
+//  1024 x  4096 x  4096   22/30      16/19      20/27      29/41
+//  2048 x 14336 x  4096  121/189     77/104     64/89      88/120
+//  6783 x  4096 x 14336  487/631    354/409    278/347    223/294
+// (fp32 y from 8-bit rows, whose codes are decoded: 256 x 4096 x 4096 16.8 us with 64x64,
+// 6783 x 4096 x 14336 665 us with 256x128.)
 #pragma once
 
 #include <stddef.h>
@@ -15,87 +28,113 @@ namespace lora {
 // an activation row.
 constexpr int mx_step(int bits) { return bits == 4 ? 256 : 128; }
 
+// A row's scales are loaded for several steps at a time, since a load fetches a whole
+// line of memory for each row however little of it is wanted: the words of kSpan steps,
+// for a kSpan-th of the rows in each step.  They lie in a ring of three such spans: one
+// that is read, one whose loads may be outstanding, and the one that the step ST later
+// loads into.
 template <int BN, int BT, int ST, int XB>
 struct MxLds {
     static constexpr int kStep = mx_step(XB);
-    static constexpr int kRowW = kStep / 2, kRowX = 128;           // bytes of a row's step
-    static constexpr int kWordsW = kStep / 128;                    // words of scales of a weight row's step
-    static constexpr int kWordsX = XB == 4 ? 2 : 1;
+    static constexpr int kRowW = kStep / 2, kRowX = 128;  // bytes of a row's step
     static constexpr int kStage = BN * kRowW + BT * kRowX;
-    static constexpr int kChunksW = (BN * kWordsW + 63) / 64, kChunksX = (BT * kWordsX + 63) / 64;  // loads of 64 words
-    static constexpr int kScales = (kChunksW + kChunksX) * 256;
-    static constexpr int kBytes = ST * kStage + (ST + 1) * kScales;
+    static constexpr int kSlots = 3;
+    static constexpr bool fits(int span) {
+        return ST * kStage + kSlots * (BN * span * kStep / 128 + BT * (XB == 4 ? span * 2 : span / 4)) * 4 <= kLdsBytes;
+    }
+    static constexpr int kSpan = XB == 8 ? (fits(8) ? 8 : 4) : fits(4) ? 4 : 2;  // 1024 columns, or 512
+    static_assert(ST <= kSpan, "a slot was last read before its first loads go out");
+    static constexpr int kWordsW = kSpan * kStep / 128, kWordsX = XB == 4 ? kWordsW : kSpan / 4;  // of a row's span
+    static constexpr int kAllW = BN * kWordsW / 64, kAllX = BT * kWordsX / 64;                  // loads of a span, 64 words each
+    static constexpr int kLoadsW = kAllW / kSpan, kLoadsX = kAllX > kSpan ? kAllX / kSpan : 1;  // of a step
+    static_assert(kAllW % kSpan == 0 && (kAllX % kSpan == 0 || kSpan % kAllX == 0), "the loads divide evenly");
+    static constexpr int kScales = (kAllW + kAllX) * 256;
+    static constexpr int kBytes = ST * kStage + kSlots * kScales;
     static_assert(kBytes <= kLdsBytes, "a CU's LDS");
 };
 
-enum { kMxStream = 0, kMx32x64, kMx64x64, kMx64x128, kMx128x128, kMx256x128, kMx256x256, kMxKinds };
+// Kernels: tiles through LDS, and (from kMx16x16 on) tiles of waves side by side along k.
+enum { kMx64x64 = 0, kMx128x128, kMx256x128, kMx256x256, kMx16x16, kMx32x16, kMxKinds };
 struct MxTile {
-    int32_t bn, bt;
+    int32_t bn, bt;            // outputs, rows
     int32_t stages4, stages8;  // of the ring in LDS, for 4-bit and 8-bit rows
-    int32_t threads;           // of a workgroup, at most
-    // us of a workgroup: its start and end, 256 columns of k for 4-bit rows, for 8-bit rows with bf16 y and fp32 y
-    float start, step4, step8, step8_f32;
+    int32_t waves;             // of a workgroup
+    // us: a call's start and end, a workgroup's; a step of 256 columns (a piece of 512 of
+    // every wave) for 4-bit rows, 8-bit rows with bf16 y, with fp32 y; a step where several
+    // workgroups share the CU (of all of them, or of each for the last two kernels)
+    float start, tile, step[3], shared[3];
 };
-constexpr MxTile kMxTiles[kMxKinds] = {{0, 0, 0, 0, 0, 0.f, 0.f, 0.f, 0.f},
-                                       {32, 64, 6, 6, 256, 0.5f, 0.151f, 0.25f, 0.5f},
-                                       {64, 64, 4, 6, 256, 0.85f, 0.198f, 0.35f, 0.55f},
-                                       {64, 128, 4, 4, 256, 1.2f, 0.351f, 0.60f, 1.1f},
-                                       {128, 128, 3, 4, 256, 2.4f, 0.45f, 0.75f, 1.6f},
-                                       {256, 128, 3, 4, 256, 3.5f, 0.677f, 1.2f, 3.f},
-                                       {256, 256, 2, 3, 512, 3.1f, 1.122f, 2.1f, 5.8f}};
-constexpr int kMxStreamWaves = 8;
+constexpr MxTile kMxTiles[kMxKinds] = {
+    {64, 64, 4, 4, 4, 2.56f, 1.36f, {0.218f, 0.279f, 0.726f}, {0.462f, 0.706f, 1.018f}},
+    {128, 128, 4, 4, 4, 1.77f, 3.46f, {0.471f, 0.653f, 1.488f}, {0.f, 0.f, 0.f}},
+    {256, 128, 2, 4, 4, 2.59f, 4.4f, {0.777f, 1.213f, 2.885f}, {0.f, 0.f, 0.f}},
+    {256, 256, 2, 2, 8, 1.22f, 5.24f, {1.307f, 1.98f, 0.f}, {0.f, 0.f, 0.f}},
+    {16, 16, 1, 1, 4, 2.13f, 0.271f, {0.627f, 0.817f, 1.116f}, {0.067f, 0.064f, 0.119f}},
+    {32, 16, 1, 1, 4, 2.02f, 0.523f, {0.93f, 1.218f, 1.383f}, {0.122f, 0.056f, 0.191f}}};
+// (fp32 sums of decoded 8-bit rows: the 256 x 256 tile's would not fit the registers)
+constexpr bool mx_kind_on(int kind, int bits, int dtype) { return kind != kMx256x256 || bits == 4 || dtype == LORA_BF16; }
+
+// Estimated us of a call of `tiles` tiles (not counting parts of k), `steps` steps of 256
+// columns and s parts, after measurements of 1200 products and 800 experts' products of
+// random sizes (1 to 6783 rows, k 256 to 14336, 256 to 14336 outputs, each kernel and
+// split): on those that the numbers were not fitted to, the choice is 1.1% slower than the
+// best in the mean (experts' products, whose rows are spread as the router likes, 2.7%).
+inline float mx_time(int kind, int bits, int dtype, int64_t tiles, int32_t steps, int32_t s, float outputs) {
+    const MxTile& c = kMxTiles[kind];
+    const int f = bits == 4 ? 0 : dtype == LORA_BF16 ? 1 : 2;
+    const int64_t n = tiles * s;
+    const float st = (float)(s == 1 ? steps : 4 * (((steps + 3) / 4 + s - 1) / s));
+    float us = c.start;
+    if (kind >= kMx16x16) {
+        us += (float)(((steps + 1) / 2 + c.waves - 1) / c.waves) * c.step[f] + (float)n / kCus * (c.tile + st * c.shared[f]);
+    } else if (kind == kMx64x64) {  // two on a CU
+        const int64_t full = n / (2 * kCus), rest = n - full * 2 * kCus;
+        us += (float)full * (c.tile + st * c.shared[f]);
+        if (rest > 0) us += c.tile + st * (rest <= kCus ? c.step[f] : c.shared[f]);
+    } else {
+        us += (float)((n + kCus - 1) / kCus) * (c.tile + st * c.step[f]);
+    }
+    return s > 1 ? us + 2.03f + (float)s * (0.056f + outputs * 2.0e-6f) : us;
+}
 
 // bits: of the activation rows.  kind: kMxKinds if no kernel's launch holds the call.
 inline BasePlan mx_plan(int bits, int dtype, int64_t T, int64_t k, int64_t N) {
     const int32_t steps = (int32_t)((k + 255) / 256);
-    const float outputs = (float)T * (float)N;
     BasePlan best{kMxKinds, 1};
     float least = 0.f;
-    for (int kind = kMx32x64; kind < kMxKinds; ++kind) {
+    for (int kind = 0; kind < kMxKinds; ++kind) {
+        if (!mx_kind_on(kind, bits, dtype)) continue;
         const MxTile& c = kMxTiles[kind];
-        const float step = bits == 4 ? c.step4 : dtype == LORA_BF16 ? c.step8 : c.step8_f32;
-        const int64_t tiles = (int64_t)(((uint32_t)N + c.bn - 1) / c.bn) * (((uint32_t)T + c.bt - 1) / c.bt);
+        const int64_t tiles = ((N + c.bn - 1) / c.bn) * ((T + c.bt - 1) / c.bt);
         for (const int32_t s : kSplits) {
-            if (s > 1 && (s > steps || tiles * s > 2 * kCus)) break;
-            if (!grid_fits(tiles * s + 8, c.threads)) break;  // (rounded up to the XCDs)
-            const float rounds = (float)((uint64_t)(tiles * s + kCus - 1) / kCus);
-            float us = rounds * (c.start + (float)((steps + s - 1) / s) * step);
-            if (s > 1) us += 2.5f + (float)s * (0.14f + outputs * 0.97e-6f);
-            if (least == 0.f || us < least) {
+            // (parts are of whole spans of scales, up to 1024 columns)
+            if (s > 1 && (s > (steps + 3) / 4 || tiles * s > 2 * kCus || kind >= kMx16x16)) break;
+            if (!grid_fits(tiles * s + 8, c.waves * 64)) break;  // (rounded up to the XCDs)
+            const float us = mx_time(kind, bits, dtype, tiles, steps, s, (float)T * (float)N);
+            if (best.kind == kMxKinds || us < least) {
                 least = us;
                 best = BasePlan{kind, s};
             }
         }
     }
-    if (T <= kStreamRows && grid_fits((N + 15) / 16, kMxStreamWaves * 64) &&
-        (float)steps * (0.2f + 0.003f * (float)(T - 1)) + (float)N * (float)k / 50e6f < least)
-        best = BasePlan{kMxStream, 1};
     return best;
 }
 
-// Rows of a tile kind (the stream's tiles hold one operand's rows).
-constexpr int32_t mx_tile_rows(int kind) { return kind == kMxStream ? kStreamRows : kMxTiles[kind].bt; }
-
 // The experts' product of T rows over `experts` weights: how many rows each has is known
-// on the device only, so the choice goes by the mean.  *tiles_t: tiles along t, at most.
+// on the device only, so the choice goes by the mean, and half a tile more for each
+// expert.  *tiles_t: tiles along t, at most.
 inline BasePlan mx_expert_plan(int bits, int dtype, int64_t T, int64_t k, int64_t N, int64_t experts, int64_t* tiles_t) {
     const int32_t steps = (int32_t)((k + 255) / 256);
-    const int64_t used = std::min(T, experts), mean = (T + used - 1) / used;
+    const int64_t used = std::min(T, experts);
     BasePlan best{kMxKinds, 1};
     float least = 0.f;
-    for (int kind = kMxStream; kind < kMxKinds; ++kind) {
+    for (int kind = 0; kind < kMxKinds; ++kind) {
+        if (!mx_kind_on(kind, bits, dtype)) continue;
         const MxTile& c = kMxTiles[kind];
-        const int32_t bt = mx_tile_rows(kind);
-        const int64_t most = T / bt + used, tiles_n = (N + (kind == kMxStream ? 16 : c.bn) - 1) / (kind == kMxStream ? 16 : c.bn);
-        if (!grid_fits(most * tiles_n + 8, kind == kMxStream ? kMxStreamWaves * 64 : c.threads)) continue;
-        float us;
-        if (kind == kMxStream) {
-            us = (float)(tiles_n * used * ((mean + bt - 1) / bt)) / (float)(kCus * 2) * (1.f + 0.12f * (float)steps);
-        } else {
-            const float step = bits == 4 ? c.step4 : dtype == LORA_BF16 ? c.step8 : c.step8_f32;
-            const int64_t tiles = tiles_n * used * ((mean + bt - 1) / bt);
-            us = (float)((tiles + kCus - 1) / kCus) * (c.start + (float)steps * step);
-        }
+        const int64_t most = T / c.bt + used, tiles_n = (N + c.bn - 1) / c.bn;
+        if (!grid_fits(most * tiles_n + 8, c.waves * 64)) continue;
+        const float each = std::max(1.f, (float)T / (float)(used * c.bt) + 0.5f);
+        const float us = mx_time(kind, bits, dtype, (int64_t)((float)(tiles_n * used) * each), steps, 1, 0.f);
         if (best.kind == kMxKinds || us < least) {
             least = us;
             best = BasePlan{kind, 1};
@@ -104,5 +143,8 @@ inline BasePlan mx_expert_plan(int bits, int dtype, int64_t T, int64_t k, int64_
     }
     return best;
 }
+
+// (a split k has no more than 2 kCus workgroups, of 256 x 256 sums at most)
+static_assert(LORA_BASE_PRODUCT_MAX_WORKSPACE >= 2 * kCus * 256 * 256 * (int)sizeof(float), "every plan fits");
 
 }  // namespace lora
