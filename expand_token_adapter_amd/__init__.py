@@ -325,7 +325,7 @@ class _Mx:
                 raise ValueError(f"{name} must be [{rows}, >= {c}] with contiguous rows")
             if rows > 1 and (t.stride(0) % unit or t.stride(0) < t.shape[1]):
                 raise ValueError(f"the row pitch of {name} must be a multiple of {unit}")
-        self.codes, self.scales, self.device = codes, scales, codes.device
+        self.codes, self.scales, self.device, self.index = codes, scales, codes.device, codes.get_device()
         # (one row has no pitch: a slice of a wider matrix may stand at any, its own width is what counts)
         self.c = _abi.LoraQuant(codes.data_ptr(), codes.stride(0) if rows > 1 else pad // 2,
                                 scales.data_ptr(), scales.stride(0) if rows > 1 else pad // _abi.LORA_MX_BLOCK)
@@ -411,8 +411,7 @@ class ExpertSegments(Segments):
         super().__init__(tokens * k, num_experts, device)
         self.tokens, self.k = tokens, k
         self.pos = torch.full((tokens, k), -1, dtype=torch.int32, device=device)
-        self.device = self.pos.device
-        self._pos = self.pos.data_ptr()
+        self.device, self.index = self.pos.device, self.pos.get_device()
 
 
 def lora_segments_build(adapter_ids: torch.Tensor, num_adapters: int, out: Optional[Segments] = None) -> Segments:
@@ -761,38 +760,59 @@ def lora_backward_quant_workspace_bytes(dtype: torch.dtype, T_ft: int, d_in: int
     return _abi.load().lora_backward_quant_workspace_bytes(_DTYPES[dtype], T_ft, d_in, d_out, r_max)
 
 
+def _launch_on(index: int, fn, *args) -> int:
+    """fn(*args, stream) on the current stream of the device with that index, made the current device."""
+    if index == _device_index() and _raw_stream is not None:
+        return fn(*args, _raw_stream(index))
+    return _launch(torch.device("cuda", index), fn, *args)
+
+
+def _matrix(fn: str, t: torch.Tensor, name: str, rows: int, index: int):
+    """(pointer, columns, pitch, type code) of a 2-D tensor of `rows` rows, contiguous each, on the device with that index."""
+    shape, stride = t.shape, t.stride()
+    code = _DTYPES.get(t.dtype)
+    if len(shape) == 2 and stride[1] == 1 and shape[0] == rows and t.get_device() == index and code is not None:
+        return t.data_ptr(), shape[1], stride[0], code
+    _on_gpu(t)
+    _dtype_code(t)
+    _rows(t, name)
+    raise ValueError(f"{fn}: {name} must have {rows} rows on cuda:{index}, it has {shape[0]} on {t.device}")
+
+
 def lora_quant_rows_mx(x: torch.Tensor, out: Optional[MxRows] = None) -> MxRows:
     """Save rows x [T, d] (bfloat16 or float32) in microscaled 4 bits; out: buffers to fill (MxRows.empty, or a slice)."""
-    _on_gpu(x)
-    code, dev = _dtype_code(x), x.device
-    px, T, d, ldx = _rows(x, "x")
     if out is None:
-        out = MxRows.empty(T, d, dev)
+        _on_gpu(x)
+        _dtype_code(x)
+        _, T, d, _ = _rows(x, "x")
+        out = MxRows.empty(T, d, x.device)
     elif not isinstance(out, MxRows):
         raise TypeError("out must be a MxRows")
-    elif out.T != T or out.d != d or out.device != dev:
-        raise ValueError(f"out must hold {T} rows of {d} values on x's device")
-    _abi.check("lora_quant_rows_mx", _launch(dev, _abi.load().lora_quant_rows_mx, code, px, ldx, T, d, out.c))
+    px, d, ldx, code = _matrix("lora_quant_rows_mx", x, "x", out.T, out.index)
+    if d != out.d:
+        raise ValueError(f"out must hold rows of {d} values")
+    st = _launch_on(out.index, _abi.load().lora_quant_rows_mx, code, px, ldx, out.T, d, out.c)
+    if st:
+        _abi.check("lora_quant_rows_mx", st)
     return out
 
 
 def lora_dequant_rows_mx(q, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of q (MxRows, or a MxWeight's rows), as a tensor of dtype (or into out, whose type counts)."""
-    if isinstance(q, MxWeight):
-        T, d = q.d_out * (q.experts or 1), q.d_in
-    elif isinstance(q, MxRows):
+    if isinstance(q, MxRows):
         T, d = q.T, q.d
+    elif isinstance(q, MxWeight):
+        T, d = q.d_out * (q.experts or 1), q.d_in
     else:
         raise TypeError("q must be a MxRows or a MxWeight")
-    dev = q.device
     if out is None:
-        out = torch.empty(T, d, dtype=dtype, device=dev)
-    _on_gpu(out)
-    code = _dtype_code(out)
-    px, rows, cols, ldx = _rows(out, "out")
-    if rows != T or cols != d or out.device != dev:
-        raise ValueError(f"out must be [{T}, {d}] on q's device")
-    _abi.check("lora_dequant_rows_mx", _launch(dev, _abi.load().lora_dequant_rows_mx, code, q.c, T, d, px, ldx))
+        out = torch.empty(T, d, dtype=dtype, device=q.device)
+    px, cols, ldx, code = _matrix("lora_dequant_rows_mx", out, "out", T, q.index)
+    if cols != d:
+        raise ValueError(f"out must be [{T}, {d}]")
+    st = _launch_on(q.index, _abi.load().lora_dequant_rows_mx, code, q.c, T, d, px, ldx)
+    if st:
+        _abi.check("lora_dequant_rows_mx", st)
     return out
 
 
@@ -828,19 +848,21 @@ def lora_base_product_mx_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
     return _abi.load().lora_base_product_mx_workspace_bytes(T, d_in, d_out)
 
 
-def _mx_operands(fn: str, x, w, y, T_y, accumulate: bool, dtype):
-    """Checked (x_bits, y) of a product of rows x (MxRows or QuantRows) and a 4-bit weight w."""
-    if not isinstance(x, (MxRows, QuantRows)) or not isinstance(w, MxWeight):
+def _mx_operands(fn: str, x, w, y, accumulate: bool, dtype, new):
+    """Checked (x_bits, y, its pointer, pitch and type code) of a product of rows x (MxRows or QuantRows) and a 4-bit weight w."""
+    bits = 4 if isinstance(x, MxRows) else 8 if isinstance(x, QuantRows) else 0
+    if not bits or not isinstance(w, MxWeight):
         raise TypeError(f"{fn}: x must be a MxRows or a QuantRows and w a MxWeight")
-    dev = x.device
-    if x.d != w.d_in or dev != w.device:
-        raise ValueError(f"{fn}: x has {x.d} columns on {dev}, w has d_in = {w.d_in} on {w.device}")
+    if x.d != w.d_in or x.codes.get_device() != w.index:
+        raise ValueError(f"{fn}: x has {x.d} columns on {x.device}, w has d_in = {w.d_in} on {w.device}")
     if y is None:
         if accumulate:
             raise ValueError(f"{fn}: accumulate needs y")
-        y = (torch.zeros if T_y is not None else torch.empty)(x.T, w.d_out, dtype=dtype, device=dev)
-    _on_gpu(y)
-    return 4 if isinstance(x, MxRows) else 8, y
+        y = new(x.T, w.d_out, dtype=dtype, device=x.device)
+    py, d_out, ldy, code = _matrix(fn, y, "y", x.T, w.index)
+    if d_out != w.d_out:
+        raise ValueError(f"{fn}: y must be [{x.T}, {w.d_out}]")
+    return bits, y, py, ldy, code
 
 
 def lora_base_product_mx(x, w: MxWeight, y: Optional[torch.Tensor] = None, accumulate: bool = False,
@@ -850,22 +872,19 @@ def lora_base_product_mx(x, w: MxWeight, y: Optional[torch.Tensor] = None, accum
 
     Sums are fp32, rounded once.  Products are exact but for 8-bit rows with bfloat16 y, where the matrix instruction
     cuts them as in lora_base_product."""
-    bits, y = _mx_operands("lora_base_product_mx", x, w, y, None, accumulate, dtype)
+    fn = "lora_base_product_mx"
+    bits, y, py, ldy, code = _mx_operands(fn, x, w, y, accumulate, dtype, torch.empty)
     if w.experts is not None:
-        raise ValueError("lora_base_product_mx: w holds several experts' weights (lora_expert_product_mx)")
-    dev = x.device
-    code = _dtype_code(y)
-    py, T, d_out, ldy = _rows(y, "y")
-    if T != x.T or d_out != w.d_out or y.device != dev:
-        raise ValueError(f"y must be [{x.T}, {w.d_out}] on x's device")
+        raise ValueError(f"{fn}: w holds several experts' weights (lora_expert_product_mx)")
     lib = _abi.load()
     if ws is None:  # a caller's workspace is size-checked by the library (LORA_ERR_WORKSPACE)
-        ws = torch.empty(max(lib.lora_base_product_mx_workspace_bytes(T, x.d, d_out), 1), dtype=torch.uint8, device=dev)
-    elif ws.device != dev or not ws.is_contiguous():
-        raise ValueError("ws must be contiguous on x's device")
-    st = _launch(dev, lib.lora_base_product_mx, code, bits, x.c, T, x.d, w.c, d_out, py, ldy, 1 if accumulate else 0,
-                 ws.data_ptr(), ws.nbytes)
-    _abi.check("lora_base_product_mx", st)
+        ws = torch.empty(max(lib.lora_base_product_mx_workspace_bytes(x.T, x.d, w.d_out), 1), dtype=torch.uint8, device=x.device)
+    elif ws.get_device() != w.index or not ws.is_contiguous():
+        raise ValueError(f"{fn}: ws must be contiguous on x's device")
+    st = _launch_on(w.index, lib.lora_base_product_mx, code, bits, x.c, x.T, x.d, w.c, w.d_out, py, ldy, 1 if accumulate else 0,
+                    ws.data_ptr(), ws.nbytes)
+    if st:
+        _abi.check(fn, st)
     return y
 
 
@@ -875,33 +894,33 @@ def lora_expert_segments(expert_ids: torch.Tensor, num_experts: int, out: Option
     if expert_ids.dtype != torch.int32 or expert_ids.dim() != 2 or not expert_ids.is_contiguous():
         raise ValueError("expert_ids must be a contiguous 2-D int32 tensor")
     T, k = expert_ids.shape
-    dev = expert_ids.device
-    seg = out if out is not None else ExpertSegments(T, k, num_experts, dev)
+    index = expert_ids.get_device()
+    seg = out if out is not None else ExpertSegments(T, k, num_experts, expert_ids.device)
     if not isinstance(seg, ExpertSegments):
         raise TypeError("out must be an ExpertSegments")
-    if seg.tokens != T or seg.k != k or seg.num_adapters != num_experts or seg.device != dev:
+    if seg.tokens != T or seg.k != k or seg.num_adapters != num_experts or seg.index != index:
         raise ValueError("ExpertSegments buffers were sized for another batch")
-    st = _launch(dev, _abi.load().lora_expert_segments, expert_ids.data_ptr(), T, k, num_experts, seg.c, seg._pos,
-                 seg.ws.data_ptr(), seg.ws.numel())
-    _abi.check("lora_expert_segments", st)
+    st = _launch_on(index, _abi.load().lora_expert_segments, expert_ids.data_ptr(), T, k, num_experts, seg.c, seg.pos.data_ptr(),
+                    seg.ws.data_ptr(), seg.ws.nbytes)
+    if st:
+        _abi.check("lora_expert_segments", st)
     return seg
 
 
-def _expert_rows(fn: str, seg, t: torch.Tensor, name: str, rows: int, like: Optional[torch.Tensor] = None):
-    """Checked (pointer, columns, pitch) of a matrix with `rows` rows on the segments' device (and like's type and width)."""
+def _expert_segments(fn: str, seg) -> None:
     if not isinstance(seg, ExpertSegments):
         raise TypeError(f"{fn}: seg must be an ExpertSegments (lora_expert_segments)")
-    _on_gpu(t)
-    pt, n, d, ld = _rows(t, name)
-    if n != rows or t.device != seg.device:
-        raise ValueError(f"{fn}: {name} must have {rows} rows on the segments' device")
-    if like is not None and (t.dtype != like.dtype or d != like.shape[1]):
-        raise ValueError(f"{fn}: {name} must be {like.dtype} with {like.shape[1]} columns")
-    return pt, d, ld
+    if seg.index < 0:
+        raise ValueError("tensors must be on the GPU")
+
+
+def _same(fn: str, name: str, d: int, code: int, d0: int, code0: int) -> None:
+    if d != d0 or code != code0:
+        raise ValueError(f"{fn}: {name} must have {d0} columns of the same type")
 
 
 def _router_weights(fn: str, seg: ExpertSegments, w: torch.Tensor, name: str = "w") -> int:
-    if w.dtype != torch.float32 or w.dim() != 2 or w.shape != seg.pos.shape or not w.is_contiguous() or w.device != seg.device:
+    if w.dtype is not torch.float32 or w.shape != seg.pos.shape or not w.is_contiguous() or w.get_device() != seg.index:
         raise ValueError(f"{fn}: {name} must be float32 [{seg.tokens}, {seg.k}], contiguous, on the segments' device")
     return w.data_ptr()
 
@@ -910,12 +929,15 @@ def lora_expert_gather(x: torch.Tensor, seg: ExpertSegments, y: Optional[torch.T
     """y[pos[t, j]] = x[t]: every token's row at the places of its choices, sorted by expert.  y [tokens * k, d]: rows
     behind the last expert's are left as they are (zeros in a new y)."""
     fn = "lora_expert_gather"
-    px, d, ldx = _expert_rows(fn, seg, x, "x", getattr(seg, "tokens", 0))
+    _expert_segments(fn, seg)
+    px, d, ldx, code = _matrix(fn, x, "x", seg.tokens, seg.index)
     if y is None:
         y = torch.zeros(seg.T, d, dtype=x.dtype, device=x.device)
-    py, _, ldy = _expert_rows(fn, seg, y, "y", seg.T, x)
-    _abi.check(fn, _launch(seg.device, _abi.load().lora_expert_gather, _dtype_code(x), px, ldx, seg.tokens, d, seg.k, seg._pos,
-                           py, ldy))
+    py, dy, ldy, cy = _matrix(fn, y, "y", seg.T, seg.index)
+    _same(fn, "y", dy, cy, d, code)
+    st = _launch_on(seg.index, _abi.load().lora_expert_gather, code, px, ldx, seg.tokens, d, seg.k, seg.pos.data_ptr(), py, ldy)
+    if st:
+        _abi.check(fn, st)
     return y
 
 
@@ -923,14 +945,18 @@ def lora_expert_gather_backward(dy: torch.Tensor, seg: ExpertSegments, dx: Optio
                                 accumulate: bool = False) -> torch.Tensor:
     """The gather's gradient: dx[t] = sum_j dy[pos[t, j]] (accumulate: +=), in fp32, rounded once."""
     fn = "lora_expert_gather_backward"
-    pdy, d, lddy = _expert_rows(fn, seg, dy, "dy", getattr(seg, "T", 0))
+    _expert_segments(fn, seg)
+    pdy, d, lddy, code = _matrix(fn, dy, "dy", seg.T, seg.index)
     if dx is None:
         if accumulate:
             raise ValueError(f"{fn}: accumulate needs dx")
         dx = torch.empty(seg.tokens, d, dtype=dy.dtype, device=dy.device)
-    pdx, _, lddx = _expert_rows(fn, seg, dx, "dx", seg.tokens, dy)
-    _abi.check(fn, _launch(seg.device, _abi.load().lora_expert_gather_backward, _dtype_code(dy), pdy, lddy, seg.tokens, d, seg.k,
-                           seg._pos, pdx, lddx, 1 if accumulate else 0))
+    pdx, d2, lddx, c2 = _matrix(fn, dx, "dx", seg.tokens, seg.index)
+    _same(fn, "dx", d2, c2, d, code)
+    st = _launch_on(seg.index, _abi.load().lora_expert_gather_backward, code, pdy, lddy, seg.tokens, d, seg.k, seg.pos.data_ptr(),
+                    pdx, lddx, 1 if accumulate else 0)
+    if st:
+        _abi.check(fn, st)
     return dx
 
 
@@ -939,15 +965,19 @@ def lora_expert_combine(o: torch.Tensor, w: torch.Tensor, seg: ExpertSegments, y
     """y[t] = sum_j w[t, j] o[pos[t, j]] (accumulate: +=), in fp32, rounded once; o [tokens * k, d] sorted by expert,
     w [tokens, k] float32."""
     fn = "lora_expert_combine"
-    po, d, ldo = _expert_rows(fn, seg, o, "o", getattr(seg, "T", 0))
+    _expert_segments(fn, seg)
+    po, d, ldo, code = _matrix(fn, o, "o", seg.T, seg.index)
     pw = _router_weights(fn, seg, w)
     if y is None:
         if accumulate:
             raise ValueError(f"{fn}: accumulate needs y")
         y = torch.empty(seg.tokens, d, dtype=o.dtype, device=o.device)
-    py, _, ldy = _expert_rows(fn, seg, y, "y", seg.tokens, o)
-    _abi.check(fn, _launch(seg.device, _abi.load().lora_expert_combine, _dtype_code(o), po, ldo, seg.tokens, d, seg.k, seg._pos, pw,
-                           py, ldy, 1 if accumulate else 0))
+    py, dy, ldy, cy = _matrix(fn, y, "y", seg.tokens, seg.index)
+    _same(fn, "y", dy, cy, d, code)
+    st = _launch_on(seg.index, _abi.load().lora_expert_combine, code, po, ldo, seg.tokens, d, seg.k, seg.pos.data_ptr(), pw, py, ldy,
+                    1 if accumulate else 0)
+    if st:
+        _abi.check(fn, st)
     return y
 
 
@@ -957,16 +987,21 @@ def lora_expert_combine_backward(dy: torch.Tensor, o: torch.Tensor, w: torch.Ten
     choice of no expert).  Returns (d_o, dw).  Rows of d_o behind the last expert's are left as they are (zeros in a
     new d_o); d_o may be o."""
     fn = "lora_expert_combine_backward"
-    pdy, d, lddy = _expert_rows(fn, seg, dy, "dy", getattr(seg, "tokens", 0))
-    po, _, ldo = _expert_rows(fn, seg, o, "o", seg.T, dy)
+    _expert_segments(fn, seg)
+    pdy, d, lddy, code = _matrix(fn, dy, "dy", seg.tokens, seg.index)
+    po, d1, ldo, c1 = _matrix(fn, o, "o", seg.T, seg.index)
+    _same(fn, "o", d1, c1, d, code)
     pw = _router_weights(fn, seg, w)
     if d_o is None:
         d_o = torch.zeros(seg.T, d, dtype=dy.dtype, device=dy.device)
     if dw is None:
         dw = torch.empty(seg.tokens, seg.k, dtype=torch.float32, device=dy.device)
-    pd, _, ldd = _expert_rows(fn, seg, d_o, "d_o", seg.T, dy)
-    _abi.check(fn, _launch(seg.device, _abi.load().lora_expert_combine_backward, _dtype_code(dy), pdy, lddy, po, ldo, seg.tokens, d,
-                           seg.k, seg._pos, pw, pd, ldd, _router_weights(fn, seg, dw, "dw")))
+    pd, d2, ldd, c2 = _matrix(fn, d_o, "d_o", seg.T, seg.index)
+    _same(fn, "d_o", d2, c2, d, code)
+    st = _launch_on(seg.index, _abi.load().lora_expert_combine_backward, code, pdy, lddy, po, ldo, seg.tokens, d, seg.k,
+                    seg.pos.data_ptr(), pw, pd, ldd, _router_weights(fn, seg, dw, "dw"))
+    if st:
+        _abi.check(fn, st)
     return d_o, dw
 
 
@@ -978,17 +1013,15 @@ def lora_expert_product_mx(x, w: MxWeight, seg: Segments, y: Optional[torch.Tens
     fn = "lora_expert_product_mx"
     if not isinstance(seg, Segments):
         raise TypeError(f"{fn}: seg must be a Segments (lora_expert_segments)")
-    bits, y = _mx_operands(fn, x, w, y, seg.T, accumulate, dtype)
-    dev = x.device
-    code = _dtype_code(y)
-    py, T, d_out, ldy = _rows(y, "y")
-    if T != x.T or d_out != w.d_out or y.device != dev:
-        raise ValueError(f"{fn}: y must be [{x.T}, {w.d_out}] on x's device")
-    if seg.T != T or seg.num_adapters != (w.experts or 1) or seg.offsets.device != dev:
+    bits, y, py, ldy, code = _mx_operands(fn, x, w, y, accumulate, dtype, torch.zeros)
+    experts = w.experts or 1
+    if seg.T != x.T or seg.num_adapters != experts or seg.offsets.get_device() != w.index:
         raise ValueError(f"{fn}: the segments are of {seg.T} rows and {seg.num_adapters} experts on {seg.offsets.device}, the call "
-                         f"has {T} and {w.experts or 1} on {dev}")
-    _abi.check(fn, _launch(dev, _abi.load().lora_expert_product_mx, code, bits, x.c, T, x.d, w.c, w.experts or 1, d_out, seg.c, py, ldy,
-                           1 if accumulate else 0))
+                         f"has {x.T} and {experts} on {w.device}")
+    st = _launch_on(w.index, _abi.load().lora_expert_product_mx, code, bits, x.c, x.T, x.d, w.c, experts, w.d_out, seg.c, py, ldy,
+                    1 if accumulate else 0)
+    if st:
+        _abi.check(fn, st)
     return y
 
 

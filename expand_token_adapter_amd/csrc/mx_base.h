@@ -365,7 +365,8 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     auto after_slot = [](int at) { return at == (L::kSlots - 1) * L::kScales ? 0 : at + L::kScales; };
     // Step i, place q modulo its span's steps: places in the rings are known when the code is made (half
     // of a step's instructions were their arithmetic, and a wave alone on its SIMD takes a
-    // few cycles for each: 256 x 4096 x 4096 from 8-bit rows XXX).
+    // few cycles for each: 256 x 4096 x 4096 from 8-bit rows 14.0 us,
+    // and 10.8 as it is).
     auto step = [&](auto place, int i) {
         constexpr int q = decltype(place)::value, slot = q % ST, next = (q + 1) % ST;
         constexpr int part = q % L::kSpan, npart = (q + 1) % L::kSpan, lpart = (q + ST) % L::kSpan;

@@ -587,8 +587,8 @@ int lora_quant_rows_mx(int dtype, const void* x, int64_t ldx, int32_t T, int32_t
 /*
  * Restore rows: x [T, ldx] (dtype) = the values of q, d columns (exact in both
  * types; magnitudes from 2^128 up, which start at scale byte 253 and come from saved
- * ones of 1.75 * 2^127 or more, are infinite).  One kernel.  LORA_ERR_UNSUPPORTED as
- * lora_quant_rows_mx.
+ * ones of 1.75 * 2^127 or more, are infinite).  One kernel.  LORA_ERR_UNSUPPORTED for
+ * more than 2^29 - 64 units of 256 columns (LORA_F32: 2^28 - 32).
  */
 int lora_dequant_rows_mx(int dtype, lora_quant q, int32_t T, int32_t d, void* x, int64_t ldx, void* stream);
 
@@ -599,8 +599,7 @@ int lora_dequant_rows_mx(int dtype, lora_quant q, int32_t T, int32_t d, void* x,
  * weight [d_in, d_out], for products with W^T (dX = W^T dY).  A weight that is used
  * in one direction alone is better saved by lora_quant_rows_mx, with a scale of its
  * own for each row.  d_out and d_in multiples of 8.  One kernel, once per weight.
- * LORA_ERR_UNSUPPORTED for d_out above 32 * 65535 (transpose = 1: d_in above 64 *
- * 65535) and rows of more than 2^24 - 1 units of 256 columns.
+ * LORA_ERR_UNSUPPORTED for d_out (transpose = 1: d_in) above 128 * 65535.
  */
 int lora_quant_weight_mx(int dtype, const void* w, int64_t ldw, int32_t d_out, int32_t d_in, int32_t transpose,
                          lora_quant q, void* stream);

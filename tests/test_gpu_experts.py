@@ -34,12 +34,13 @@ SIZES = [(1, 1, 1, 8), (1, 8, 64, 4096), (7, 3, 5, 264), (33, 2, 8, 1160), (211,
          (1000, 2, 320, 136)]
 
 
-@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (5, 2, 3), (100, 8, 64), (3000, 4, 300), (9000, 8, 16), (700, 2, 1500)])
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (5, 2, 3), (100, 8, 64), (1024, 4, 7), (1025, 4, 7), (3000, 4, 300), (5000, 1, 1024),
+                                   (9000, 8, 16), (5003, 1, 1), (140001, 2, 33), (700, 2, 1500), (40000, 2, 1100)])
 def test_segments_and_places(T, k, E):
-    """Both builds (one workgroup, three kernels), with dropped choices and ids outside the table."""
+    """Every build (one workgroup, two kernels, three kernels), with dropped choices and ids outside the table."""
     ids = mh.random_choices(T, k, E, T + E)
     if T > 4:
-        ids[3, 0], ids[4, 1] = E, -7
+        ids[3, 0], ids[4, -1] = E, -7
     seg = lb.lora_expert_segments(torch.from_numpy(ids).cuda(), E)
     off, perm, pos = mh.sort_choices(ids, E)
     assert np.array_equal(seg.offsets.cpu().numpy(), off)
@@ -47,7 +48,7 @@ def test_segments_and_places(T, k, E):
     assert np.array_equal(seg.pos.cpu().numpy(), pos)
     assert int(seg.err.item()) == (2 if T > 4 else 0)
     plain = lb.lora_segments_build(torch.from_numpy(ids.reshape(-1).copy()).cuda(), E)
-    for name in ("counts", "offsets"):
+    for name in ("counts", "offsets", "sched", "err"):
         assert torch.equal(getattr(seg, name), getattr(plain, name))
     again = lb.lora_expert_segments(torch.full((T, k), -1, dtype=torch.int32, device="cuda"), E, out=seg)
     assert again is seg and (seg.pos == -1).all() and (seg.offsets == 0).all()

@@ -57,7 +57,7 @@ def test_weight_refusals(lib):
     for kw, want in BAD_MX:
         assert call(q=_q(**kw)) == want, kw
         assert call(tr=1, q=_q(**kw)) == want, kw
-    assert call(n=2 ** 21 + 8) == UNS and call(tr=1, k=2 ** 22 + 8, ldw=2 ** 22 + 8) == UNS
+    assert call(n=2 ** 23 + 8) == UNS and call(tr=1, k=2 ** 23 + 8, ldw=2 ** 23 + 8) == UNS
 
 
 def _q8():
