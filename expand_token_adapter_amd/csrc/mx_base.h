@@ -18,8 +18,12 @@
 // 8-bit rows: products of a group of 8 columns are cut as in base.h (measured: beside
 // 4 * 256, 2^-3 is kept and 2^-4 lost, also in sevens; 0.5 * 256 counts as 1 * 256,
 // as a subnormal 8-bit code counts as 2^-6).  bf16 y takes it: 1.5e-5 of a result on
-// normal data.  fp32 y takes exact products of the values as bf16 numbers, as base.h
-// does.
+// normal data.  fp32 y takes the rows' codes in two halves, those of 2 and more and the
+// smaller ones, so that nothing is cut: the products of the first are multiples of 2^-2 *
+// 0.5 and their powers of two up to 2^(8 + 2), of which 2^-13 is 2^-3; those of the
+// second multiples of 2^-9 * 0.5, with up to 2^(0 + 2), of which 2^-13 is 2^-11.  A code's
+// half is its bit 6.  (Codes decoded to bf16 numbers, for that instruction, cost as much
+// of the matrix cores and more vector work: 2048 x 14336 x 4096 175 us against 162.)
 //
 // A operand = weight rows (n), B operand = activation rows (t), blocks of weight rows
 // in pairs so that a lane ends with eight consecutive n of one t, as in base.h.
@@ -114,13 +118,25 @@ __device__ __forceinline__ MxGroup mx_find_tile(const MxParams& p, int tile, int
 
 // ------------------------------------------------------------------ operands
 
-// Whether a product's codes are decoded to bf16 numbers (XB: bits of the activation
-// rows, DT: type of y).
+// Whether the rows' codes are taken in two halves (XB: bits of the activation rows, DT:
+// type of y).
 template <int XB, int DT>
-constexpr bool kMxDecode = XB == 8 && DT == LORA_F32;
+constexpr bool kMxHalves = XB == 8 && DT == LORA_F32;
+
+// Four 8-bit codes' upper half: the codes of magnitude 2 and more, zeros for the others.
+__device__ __forceinline__ uint32_t mx_upper(uint32_t w) {
+    // (bit 6 of every byte spread over it: the selectors 8 to 11 give the signs of bytes 1
+    // and 3 of the second and the first operand)
+    return w & __builtin_amdgcn_perm(w << 1, w << 9, 0x0b090a08u);
+}
+__device__ __forceinline__ u32x4_t mx_upper(u32x4_t q) { return u32x4_t{mx_upper(q[0]), mx_upper(q[1]), mx_upper(q[2]), mx_upper(q[3])}; }
 
 // 32 4-bit codes as the matrix instruction's operand.
 __device__ __forceinline__ i32x8_t mx_operand(u32x4_t q) { return i32x8_t{(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0}; }
+// 32 8-bit codes.
+__device__ __forceinline__ i32x8_t mx_operand(u32x4_t a, u32x4_t b) {
+    return __builtin_bit_cast(i32x8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
 
 // ------------------------------------------------------------------ tiles through LDS
 //
@@ -138,7 +154,7 @@ __device__ __forceinline__ i32x8_t mx_operand(u32x4_t q) { return i32x8_t{(int)q
 template <int BN, int BT, int WN, int WT, int ST, int XB, int DT>
 __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     using L = MxLds<BN, BT, ST, XB>;
-    constexpr bool kDecode = kMxDecode<XB, DT>;
+    constexpr bool kHalves = kMxHalves<XB, DT>;
     constexpr int NW = WN * WT;
     constexpr int FN = BN / WN / 16, FT = BT / WT / 16;  // 16 x 16 blocks of a wave
     constexpr int SUB = XB == 4 ? 2 : 1;                 // instructions of a step and block
@@ -289,11 +305,8 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     // This lane's units of an operand row.  Weight row of operand row lr: 8 (lr / 4) +
     // lr % 4 of the pair of blocks, + 4 for its second block.
     const int lrow_w = (8 * (lr >> 2) + (lr & 3)) * L::kRowW + (L::kRowW == 128 ? (lg ^ (lr & 7)) * 16 : (lg ^ ((lr >> 1) & 3)) * 16);
-    // 8-bit rows: units lg and lg + 4 (the instruction's columns), or 2 lg and 2 lg + 1
-    // where the codes are decoded (the weight's columns); 4-bit rows: lg and lg + 4
-    const int lrow_x = lr * L::kRowX + (((kDecode ? 2 * lg : lg) ^ (lr & 7)) * 16);
-    constexpr int kOther = kDecode ? 16 : 64;
-    u32x4_t a[2][GA][SUB], b[FT][2];
+    const int lrow_x = lr * L::kRowX + ((lg ^ (lr & 7)) * 16);  // (and 64 bytes on)
+    u32x4_t a[2][GA][SUB], b[FT][2], upper[kHalves ? FT : 1][2];
     constexpr int SX = XB == 4 ? 2 : 1;
     uint32_t wsc[2][GA][SUB], xsc[FT][SX];
     auto read_a = [&](int buf, int f, int u, int slot, int g) {
@@ -314,7 +327,7 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
     };
     auto read_b = [&](int h, int u, int slot) {
         b[h][u] = *reinterpret_cast<const u32x4_t*>(s_lds + slot * L::kStage + BN * L::kRowW + (wt + 16 * h) * L::kRowX +
-                                                    (u ? lrow_x ^ kOther : lrow_x));
+                                                    (u ? lrow_x ^ 64 : lrow_x));
     };
     auto read_xs = [&](int h, const char* at, int part) {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(at + (wt + 16 * h) * L::kWordsX * 4 +
@@ -390,15 +403,6 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
             uint32_t as[GA];
 #pragma unroll
             for (int f = 0; f < GA; ++f) as[f] = pick(wsc[cur][f]);
-            Frag<LORA_BF16> aq[kDecode ? GA : 1][4];
-            if constexpr (kDecode) {
-#pragma unroll
-                for (int f = 0; f < GA; ++f) {
-                    const float s = quant_scale(as[f] & 255u);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) aq[f][c] = mx_decode8<LORA_BF16>(a[cur][f][0][c], s);
-                }
-            }
 #pragma unroll
             for (int h = 0; h < FT; ++h) {
                 if constexpr (XB == 4) {
@@ -417,25 +421,31 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
                     }
                 } else {
                     const uint32_t bs = xsc[h][0] >> (8 * (part & 3));
-                    if constexpr (kDecode) {
-                        const float s = quant_scale(bs & 255u);
-                        const Frag<LORA_BF16> bq[4] = {dequant8<LORA_BF16>(b[h][0][0], b[h][0][1], s),
-                                                       dequant8<LORA_BF16>(b[h][0][2], b[h][0][3], s),
-                                                       dequant8<LORA_BF16>(b[h][1][0], b[h][1][1], s),
-                                                       dequant8<LORA_BF16>(b[h][1][2], b[h][1][3], s)};
+                    if constexpr (kHalves) {
+                        if constexpr (g == 0) {
 #pragma unroll
-                        for (int f = 0; f < GA; ++f)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) acc[GA * g + f][h] = mma(aq[f][c], bq[c], acc[GA * g + f][h]);
-                    } else {
-                        const i32x8_t bo = __builtin_bit_cast(
-                            i32x8_t, __builtin_shufflevector(b[h][0], b[h][1], 0, 1, 2, 3, 4, 5, 6, 7));
+                            for (int u = 0; u < 2; ++u) {
+                                upper[h][u] = mx_upper(b[h][u]);
+                                b[h][u] ^= upper[h][u];
+                                // (both now: else the compiler makes the lower half in the upper's
+                                // registers, once the products that read them are done)
+                                asm volatile("" : "+v"(upper[h][u]), "+v"(b[h][u]));
+                            }
+                        }
+                        const i32x8_t bu = mx_operand(upper[h][0], upper[h][1]);
 #pragma unroll
                         for (int f = 0; f < GA; ++f) {
                             f32x4_t& c = acc[GA * g + f][h];
-                            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(a[cur][f][0]), bo, c, 4, 0, 0,
+                            c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(a[cur][f][0]), bu, c, 4, 0, 0,
                                                                                  (int)as[f], 0, (int)bs);
                         }
+                    }
+                    const i32x8_t bo = mx_operand(b[h][0], b[h][1]);
+#pragma unroll
+                    for (int f = 0; f < GA; ++f) {
+                        f32x4_t& c = acc[GA * g + f][h];
+                        c = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(a[cur][f][0]), bo, c, 4, 0, 0, (int)as[f], 0,
+                                                                             (int)bs);
                     }
                 }
                 // reads of the next group (with the last group the next step's first and its
@@ -530,7 +540,7 @@ __global__ __launch_bounds__(WN* WT* kWave) void mx_kernel(MxParams p) {
 // columns past the end lie past their buffer: nothing is fetched for them.
 template <int NW, int FN, int FT, int XB, int DT>
 __global__ __launch_bounds__(NW* kWave) void mx_stream_kernel(MxParams p) {
-    constexpr bool kDecode = kMxDecode<XB, DT>;
+    constexpr bool kHalves = kMxHalves<XB, DT>;
     constexpr int XH = XB == 4 ? 1 : 2;  // 16-byte units of a lane for 128 columns of an activation row
     __shared__ f32x4_t s_acc[NW][FN * FT][kWave];
     const int wave = wave_id();
@@ -576,7 +586,7 @@ __global__ __launch_bounds__(NW* kWave) void mx_stream_kernel(MxParams p) {
     }
 #pragma unroll
     for (int h = 0; h < FT; ++h) {
-        vx[h] = (uint32_t)((16 * h + lr) * p.ldx) + (kDecode ? 32u : 16u) * lg;
+        vx[h] = (uint32_t)((16 * h + lr) * p.ldx) + 16u * lg;
         vxs[h] = (uint32_t)((16 * h + lr) * p.ldxs);
     }
     f32x4_t acc[FN][FT];
@@ -609,7 +619,7 @@ __global__ __launch_bounds__(NW* kWave) void mx_stream_kernel(MxParams p) {
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int u = 0; u < XH; ++u)
-                    r.b[h][XH * i + u] = buf_load16(rx, vx[h] + (uint32_t)(XB * 16 * i + (kDecode ? 16 : 64) * u), 0u);
+                    r.b[h][XH * i + u] = buf_load16(rx, vx[h] + (uint32_t)(XB * 16 * i + 64 * u), 0u);
             if constexpr (XB == 4)
                 r.bs[h] = buf_load16(rxs, vxs[h], 0u);
             else
@@ -625,42 +635,31 @@ __global__ __launch_bounds__(NW* kWave) void mx_stream_kernel(MxParams p) {
             for (int f = 0; f < FN; ++f) as[f] = r.as[f][i] >> (8 * lg);
 #pragma unroll
             for (int h = 0; h < FT; ++h) bs[h] = XB == 4 ? r.bs[h][i] >> (8 * lg) : r.bs[h][0] >> (8 * i);
-            if constexpr (kDecode) {
-                Frag<LORA_BF16> bq[FT][4];
 #pragma unroll
-                for (int h = 0; h < FT; ++h) {
-                    const float s = quant_scale(bs[h] & 255u);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const u32x4_t q = r.b[h][XH * i + c / 2];
-                        bq[h][c] = dequant8<LORA_BF16>(q[2 * (c & 1)], q[2 * (c & 1) + 1], s);
+            for (int h = 0; h < FT; ++h) {
+                i32x8_t bo, bu;
+                if constexpr (XB == 4) {
+                    bo = mx_operand(r.b[h][i]);
+                } else {
+                    const u32x4_t q0 = r.b[h][XH * i], q1 = r.b[h][XH * i + XH - 1];
+                    if constexpr (kHalves) {
+                        u32x4_t u0 = mx_upper(q0), u1 = mx_upper(q1), l0 = q0 ^ u0, l1 = q1 ^ u1;
+                        asm volatile("" : "+v"(u0), "+v"(u1), "+v"(l0), "+v"(l1));  // (as in mx_kernel)
+                        bu = mx_operand(u0, u1);
+                        bo = mx_operand(l0, l1);
+                    } else {
+                        bo = mx_operand(q0, q1);
                     }
                 }
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
-                    const float s = quant_scale(as[f] & 255u);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const Frag<LORA_BF16> aq = mx_decode8<LORA_BF16>(r.a[f][i][c], s);
-#pragma unroll
-                        for (int h = 0; h < FT; ++h) acc[f][h] = mma(aq, bq[h][c], acc[f][h]);
-                    }
+                    constexpr int kFormat = XB == 4 ? 4 : 0;
+                    if constexpr (kHalves)
+                        acc[f][h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(r.a[f][i]), bu, acc[f][h], 4, kFormat, 0,
+                                                                                     (int)as[f], 0, (int)bs[h]);
+                    acc[f][h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(r.a[f][i]), bo, acc[f][h], 4, kFormat, 0,
+                                                                                 (int)as[f], 0, (int)bs[h]);
                 }
-            } else {
-#pragma unroll
-                for (int f = 0; f < FN; ++f)
-#pragma unroll
-                    for (int h = 0; h < FT; ++h) {
-                        if constexpr (XB == 4) {
-                            acc[f][h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                mx_operand(r.a[f][i]), mx_operand(r.b[h][i]), acc[f][h], 4, 4, 0, (int)as[f], 0, (int)bs[h]);
-                        } else {
-                            const i32x8_t bo = __builtin_bit_cast(
-                                i32x8_t, __builtin_shufflevector(r.b[h][XH * i], r.b[h][XH * i + XH - 1], 0, 1, 2, 3, 4, 5, 6, 7));
-                            acc[f][h] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx_operand(r.a[f][i]), bo, acc[f][h], 4, 0, 0,
-                                                                                         (int)as[f], 0, (int)bs[h]);
-                        }
-                    }
             }
         }
     };

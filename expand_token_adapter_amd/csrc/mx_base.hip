@@ -33,9 +33,12 @@ int launch_mx(MxParams p, const BasePlan& b, int64_t tiles_t, hipStream_t st) {
     p.tiles_n = (p.N + c.bn - 1) / c.bn;
     p.tiles_t = (int32_t)tiles_t;
     const unsigned grid = (unsigned)round_up(p.tiles_n * tiles_t * p.splits, kNumXcd);
+    // (rows in halves: no two waves share an activation row, whose codes each would take
+    // apart: 256 x 4096 x 4096 16.1 us in place of 18.7; in one piece 10.0 against 9.7)
+    constexpr int WN = kMxHalves<XB, DT> ? 1 : 2;
     switch (b.kind) {
-        case kMx64x64: launch_tiles<XB, DT, kMx64x64, 2, 2>(p, grid, st); break;
-        case kMx128x128: launch_tiles<XB, DT, kMx128x128, 2, 2>(p, grid, st); break;
+        case kMx64x64: launch_tiles<XB, DT, kMx64x64, WN, 4 / WN>(p, grid, st); break;
+        case kMx128x128: launch_tiles<XB, DT, kMx128x128, WN, 4 / WN>(p, grid, st); break;
         case kMx256x128: launch_tiles<XB, DT, kMx256x128, 2, 2>(p, grid, st); break;
         case kMx256x256:
             if constexpr (mx_kind_on(kMx256x256, XB, DT)) launch_tiles<XB, DT, kMx256x256, 2, 4>(p, grid, st);

@@ -11,8 +11,8 @@
 //  1024 x  4096 x  4096   22/30      16/19      20/27      29/41
 //  2048 x 14336 x  4096  121/189     77/104     64/89      88/120
 //  6783 x  4096 x 14336  487/631    354/409    278/347    223/294
-// (fp32 y from 8-bit rows, whose codes are decoded: 256 x 4096 x 4096 16.8 us with 64x64,
-// 6783 x 4096 x 14336 665 us with 256x128.)
+// (fp32 y from 8-bit rows, taken in two halves: 256 x 4096 x 4096 16.1 us with 64x64,
+// 6783 x 4096 x 14336 620 us with 256x128.)
 #pragma once
 
 #include <stddef.h>
@@ -65,13 +65,13 @@ struct MxTile {
     float start, tile, step[3], shared[3];
 };
 constexpr MxTile kMxTiles[kMxKinds] = {
-    {64, 64, 4, 4, 4, 2.56f, 1.36f, {0.218f, 0.279f, 0.726f}, {0.462f, 0.706f, 1.018f}},
-    {128, 128, 4, 4, 4, 1.77f, 3.46f, {0.471f, 0.653f, 1.488f}, {0.f, 0.f, 0.f}},
-    {256, 128, 2, 4, 4, 2.59f, 4.4f, {0.777f, 1.213f, 2.885f}, {0.f, 0.f, 0.f}},
+    {64, 64, 4, 4, 4, 2.56f, 1.36f, {0.218f, 0.279f, 0.64f}, {0.462f, 0.706f, 0.9f}},
+    {128, 128, 4, 4, 4, 1.77f, 3.46f, {0.471f, 0.653f, 1.42f}, {0.f, 0.f, 0.f}},
+    {256, 128, 2, 4, 4, 2.59f, 4.4f, {0.777f, 1.213f, 2.65f}, {0.f, 0.f, 0.f}},
     {256, 256, 2, 2, 8, 1.22f, 5.24f, {1.307f, 1.98f, 0.f}, {0.f, 0.f, 0.f}},
     {16, 16, 1, 1, 4, 2.13f, 0.271f, {0.627f, 0.817f, 1.116f}, {0.067f, 0.064f, 0.119f}},
     {32, 16, 1, 1, 4, 2.02f, 0.523f, {0.93f, 1.218f, 1.383f}, {0.122f, 0.056f, 0.191f}}};
-// (fp32 sums of decoded 8-bit rows: the 256 x 256 tile's would not fit the registers)
+// (fp32 sums of 8-bit rows' halves: the 256 x 256 tile's would not fit the registers)
 constexpr bool mx_kind_on(int kind, int bits, int dtype) { return kind != kMx256x256 || bits == 4 || dtype == LORA_BF16; }
 
 // Estimated us of a call of `tiles` tiles (not counting parts of k), `steps` steps of 256

@@ -616,12 +616,10 @@ size_t lora_base_product_mx_workspace_bytes(int32_t T, int32_t d_in, int32_t d_o
  *   lora_quant_rows (x_bits = 8); w: mx form of the weight [d_out, d_in]; y [T, ldy]
  *   (dtype).  The sums (and y_t before, if added to) are fp32 and rounded once to y's
  *   type.  What they sum:
- *   x_bits = 4  exact products, for either dtype.
- *   x_bits = 8  LORA_F32: exact products of the values as bf16 numbers (for the 8-bit
- *          rows' scale bytes from 3 to 246; as in lora_base_product).  LORA_BF16:
- *          products cut as in lora_base_product, each of the 8 of columns 8 i ..
- *          8 i + 7 below 2^-13 of the power of two of the largest, with W_k =
- *          max(|w_k|, s) in its bound (0 for w_k = 0), s the scale of w_k's block.
+ *   LORA_F32, and LORA_BF16 with x_bits = 4: exact products.
+ *   LORA_BF16 with x_bits = 8: products cut as in lora_base_product, each of the 8 of
+ *          columns 8 i .. 8 i + 7 below 2^-13 of the power of two of the largest, with
+ *          W_k = max(|w_k|, s) in its bound (0 for w_k = 0), s the scale of w_k's block.
  *   ws: lora_base_product_mx_workspace_bytes(T, d_in, d_out) bytes.
  * Rows are independent, and the order of every sum is fixed by the shapes, as in
  * lora_base_product, and so are its refusals (pitches of scales included).

@@ -231,6 +231,27 @@ def test_product_reads_nothing_past_its_columns(bits):
     assert torch.equal(lb.lora_base_product_mx(x2, w2), want)
 
 
+@pytest.mark.parametrize("T", [3, 70])
+def test_fp32_products_of_8_bit_rows_are_exact(T):
+    """Products 2^21 apart in one group of eight columns, every code in each place, at the ends of the scales: sums of a
+    few terms that fp32 holds exactly come out exact."""
+    rng = np.random.default_rng(4)
+    k, n = 256, 40
+    for xs, ws in ((127, 127), (0, 200), (250, 20)):
+        xc = rng.integers(0, 127, size=(T, k)).astype(np.uint8)
+        xc |= (rng.integers(0, 2, size=(T, k)) << 7).astype(np.uint8)
+        keep = np.zeros((n, k), bool)
+        wc = np.zeros((n, k), np.uint8)
+        for i in range(n):  # two columns of one group of eight: one addition, of numbers of at most 22 bits together
+            c = 8 * rng.integers(0, k // 8) + rng.permutation(8)[:2]
+            keep[i, c] = True
+            wc[i, c] = rng.integers(1, 16, size=2)
+        w = lb.MxWeight(torch.from_numpy(mh.pack(wc)).cuda(), torch.full((n, k // 32), ws, dtype=torch.uint8).cuda(), n, k)
+        x = lb.QuantRows(torch.from_numpy(xc).cuda(), torch.full((T, 4), xs, dtype=torch.uint8).cuda(), k)
+        want = qh.values(xc, np.full((T, 2), xs, np.uint8), k) @ mh.values(wc, np.full((n, k // 32), ws, np.uint8), k).T
+        assert np.array_equal(_f64(lb.lora_base_product_mx(x, w, dtype=torch.float32)), want), (xs, ws)
+
+
 def test_scales_at_the_ends_of_their_range():
     for bits, dt in ((4, torch.float32), (8, torch.float32), (4, torch.bfloat16), (8, torch.bfloat16)):
         for T in (4, 40):
