@@ -8,9 +8,9 @@
 // Why 6 and not a rule on the exponent alone (the largest magnitude's exponent
 // minus 2): with that one, magnitudes from 6 to 8 times the scale would be cut to
 // 6, up to a quarter of the largest value lost; here the largest is off by at most
-// a fifth (5 is stored as 4), for one binade less at the small end of such blocks.  A power of two, because the matrix instruction takes exponent bytes
-// for exactly such blocks (a lane's 32 codes of one row), so they cost a product
-// no arithmetic.
+// a fifth (5 is stored as 4), for one binade less at the small end of such blocks.  A
+// power of two, because the matrix instruction takes exponent bytes for exactly such
+// blocks (a lane's 32 codes of one row), so they cost a product no arithmetic.
 //
 // There is no 4-bit NaN: a block with a value that is not finite has the scale
 // byte 255, and all of its values are NaN.

@@ -599,7 +599,8 @@ int lora_dequant_rows_mx(int dtype, lora_quant q, int32_t T, int32_t d, void* x,
  * weight [d_in, d_out], for products with W^T (dX = W^T dY).  A weight that is used
  * in one direction alone is better saved by lora_quant_rows_mx, with a scale of its
  * own for each row.  d_out and d_in multiples of 8.  One kernel, once per weight.
- * LORA_ERR_UNSUPPORTED for d_out (transpose = 1: d_in) above 128 * 65535.
+ * LORA_ERR_UNSUPPORTED for d_out above 128 * 65535 (transpose = 1: d_in above
+ * 64 * 65535).
  */
 int lora_quant_weight_mx(int dtype, const void* w, int64_t ldw, int32_t d_out, int32_t d_in, int32_t transpose,
                          lora_quant q, void* stream);

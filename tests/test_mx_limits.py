@@ -156,3 +156,10 @@ def test_products_of_very_many_rows_or_outputs_fit_a_launch(plan, lib):
             assert got == _abi.LORA_ERR_UNSUPPORTED
             held = T * n * (4 if dt == "f32" else 2) + (T * 132 + max(1, e) * n * 136) * -(-k // 256)
             assert held > 288e9  # more than a GPU holds
+
+
+def test_weights_of_more_rows_than_a_launch_are_refused(lib):
+    """The documented limits; one row more is refused before anything is enqueued."""
+    for transpose, most in ((0, 128 * 65535), (1, 64 * 65535)):
+        n, k = (8, most + 8) if transpose else (most + 8, 8)
+        assert lib.lora_quant_weight_mx(0, FAKE, k, n, k, transpose, _q(128, 8), None) == _abi.LORA_ERR_UNSUPPORTED
