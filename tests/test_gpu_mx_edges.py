@@ -150,3 +150,25 @@ def test_work_on_another_stream_than_the_tensors():
         got = run()
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,k,d", [(1023, 2, 72), (1024, 2, 72), (1500, 9, 1032), (1100, 3, 2040), (1100, 3, 2048)])
+def test_gradients_of_the_combine_for_many_tokens(T, k, d, dtype):
+    """A wave or four waves a token, more choices than are taken at a time, tokens that do not fill a workgroup."""
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    seg = lb.lora_expert_segments(torch.from_numpy(mh.random_choices(T, k, 5, 3, drop=0.1)).cuda(), 5)
+    n, pos = int(seg.offsets[-1]), seg.pos.long()
+    dy = torch.randn(T, d, generator=g, device="cuda").to(dtype)
+    o = torch.randn(T * k, d, generator=g, device="cuda").to(dtype)
+    o[n:] = float("nan")  # of no choice
+    w = torch.randn(T, k, generator=g, device="cuda")
+    d_o, dw = lb.lora_expert_combine_backward(dy, o, w, seg, d_o=torch.full_like(o, 7))
+    on, at = pos >= 0, pos.clamp(min=0)
+    assert (d_o[n:] == 7).all() and not dw[~on].any()
+    want = (w.unsqueeze(-1) * dy.float().unsqueeze(1)).to(dtype)
+    assert torch.equal(d_o[at[on]], want[on])
+    # fp32 sums of a lane's columns, then over its wave and the workgroup: d terms, each rounding 2^-24 of what is added so far
+    rows = torch.nan_to_num(o.double())[at]
+    exact, mag = (dy.double().unsqueeze(1) * rows).sum(-1), (dy.double().unsqueeze(1) * rows).abs().sum(-1)
+    assert ((dw.double() - exact).abs()[on] <= (d / 64 + 16) * 2.0 ** -24 * mag[on]).all()
