@@ -408,10 +408,20 @@ class ExpertSegments(Segments):
     [tokens, k], the place of every choice among the sorted rows (-1: of no expert)."""
 
     def __init__(self, tokens: int, k: int, num_experts: int, device: torch.device):
-        super().__init__(tokens * k, num_experts, device)
-        self.tokens, self.k = tokens, k
-        self.pos = torch.full((tokens, k), -1, dtype=torch.int32, device=device)
+        # (one buffer, cleared at once, in place of a tensor and a launch each: a batch of its own shape needs its own
+        # segments; every part begins at 16 bytes)
+        lib = _abi.load()
+        T = tokens * k
+        elems = [num_experts, num_experts + 1, max(T, 1), 1, max(1, lib.lora_segments_sched_elems(T, num_experts)), T]
+        parts = torch.zeros(sum((n + 3) // 4 * 4 for n in elems), dtype=torch.int32, device=device).split(
+            [m for n in elems for m in (n, -n % 4)])
+        self.T, self.num_adapters, self.tokens, self.k = T, num_experts, tokens, k
+        self.counts, self.offsets, self.perm, self.err, self.sched = parts[:10:2]
+        self.pos = parts[10].view(tokens, k).fill_(-1)
+        self.ws = torch.empty(max(1, lib.lora_segments_workspace_bytes(T, num_experts)), dtype=torch.uint8, device=device)
         self.device, self.index = self.pos.device, self.pos.get_device()
+        self._c = _abi.LoraSegments(self.counts.data_ptr(), self.offsets.data_ptr(), self.perm.data_ptr(),
+                                    self.err.data_ptr(), self.sched.data_ptr())
 
 
 def lora_segments_build(adapter_ids: torch.Tensor, num_adapters: int, out: Optional[Segments] = None) -> Segments:
