@@ -23,7 +23,7 @@
 // 0.5 and their powers of two up to 2^(8 + 2), of which 2^-13 is 2^-3; those of the
 // second multiples of 2^-9 * 0.5, with up to 2^(0 + 2), of which 2^-13 is 2^-11.  A code's
 // half is its bit 6.  (Codes decoded to bf16 numbers, for that instruction, cost as much
-// of the matrix cores and more vector work: 2048 x 14336 x 4096 175 us against 162.)
+// of the matrix cores and more vector work: 2048 x 14336 x 4096 175 us against 162, in 256 x 128 tiles of four waves.)
 //
 // A operand = weight rows (n), B operand = activation rows (t), blocks of weight rows
 // in pairs so that a lane ends with eight consecutive n of one t, as in base.h.

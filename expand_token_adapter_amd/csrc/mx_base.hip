@@ -14,7 +14,7 @@ namespace {
 template <int XB, int DT, int KIND, int WN, int WT>
 void launch_tiles(const MxParams& p, unsigned grid, hipStream_t st) {
     constexpr MxTile c = kMxTiles[KIND];
-    static_assert(WN * WT <= c.waves, "the plan's bound on the launch");
+    static_assert(WN * WT == mx_waves(KIND, XB, DT), "the plan's bound on the launch");
     hipLaunchKernelGGL((mx_kernel<c.bn, c.bt, WN, WT, XB == 4 ? c.stages4 : c.stages8, XB, DT>), dim3(grid), dim3(WN * WT * kWave), 0,
                        st, p);
 }
@@ -33,13 +33,17 @@ int launch_mx(MxParams p, const BasePlan& b, int64_t tiles_t, hipStream_t st) {
     p.tiles_n = (p.N + c.bn - 1) / c.bn;
     p.tiles_t = (int32_t)tiles_t;
     const unsigned grid = (unsigned)round_up(p.tiles_n * tiles_t * p.splits, kNumXcd);
-    // (rows in halves: no two waves share an activation row, whose codes each would take
-    // apart: 256 x 4096 x 4096 16.1 us in place of 18.7; in one piece 10.0 against 9.7)
-    constexpr int WN = kMxHalves<XB, DT> ? 1 : 2;
+    // Rows in halves: in the smallest tile no two waves share an activation row, whose codes
+    // each would take apart (256 x 4096 x 4096 16.1 us in place of 18.7; in one piece 10.0
+    // against 9.7); the larger ones have two waves on a SIMD, one to take codes apart while
+    // the other multiplies (128 x 128 outputs x rows a tile: 256 x 4096 x 4096 30.3 -> 26.5 us,
+    // 2048 x 14336 x 4096 204 -> 195; 256 x 128: 49.7 -> 44.2, 184 -> 175; in one piece
+    // 119 -> 122, 103 -> 108).
+    constexpr bool kHalves = kMxHalves<XB, DT>;
     switch (b.kind) {
-        case kMx64x64: launch_tiles<XB, DT, kMx64x64, WN, 4 / WN>(p, grid, st); break;
-        case kMx128x128: launch_tiles<XB, DT, kMx128x128, WN, 4 / WN>(p, grid, st); break;
-        case kMx256x128: launch_tiles<XB, DT, kMx256x128, 2, 2>(p, grid, st); break;
+        case kMx64x64: launch_tiles<XB, DT, kMx64x64, kHalves ? 1 : 2, kHalves ? 4 : 2>(p, grid, st); break;
+        case kMx128x128: launch_tiles<XB, DT, kMx128x128, 2, kHalves ? 4 : 2>(p, grid, st); break;
+        case kMx256x128: launch_tiles<XB, DT, kMx256x128, 2, kHalves ? 4 : 2>(p, grid, st); break;
         case kMx256x256:
             if constexpr (mx_kind_on(kMx256x256, XB, DT)) launch_tiles<XB, DT, kMx256x256, 2, 4>(p, grid, st);
             break;

@@ -12,7 +12,8 @@
 //  2048 x 14336 x  4096  121/189     77/104     64/89      88/120
 //  6783 x  4096 x 14336  487/631    354/409    278/347    223/294
 // (fp32 y from 8-bit rows, taken in two halves: 256 x 4096 x 4096 16.1 us with 64x64,
-// 6783 x 4096 x 14336 620 us with 256x128.)
+// 2048 x 14336 x 4096 174 and
+// 6783 x 4096 x 14336 655 with 256x128.)
 #pragma once
 
 #include <stddef.h>
@@ -58,27 +59,33 @@ enum { kMx64x64 = 0, kMx128x128, kMx256x128, kMx256x256, kMx16x16, kMx32x16, kMx
 struct MxTile {
     int32_t bn, bt;            // outputs, rows
     int32_t stages4, stages8;  // of the ring in LDS, for 4-bit and 8-bit rows
-    int32_t waves;             // of a workgroup
+    int32_t waves;             // of a workgroup (mx_waves)
     // us: a call's start and end, a workgroup's; a step of 256 columns (a piece of 512 of
     // every wave) for 4-bit rows, 8-bit rows with bf16 y, with fp32 y; a step where several
     // workgroups share the CU (of all of them, or of each for the last two kernels)
     float start, tile, step[3], shared[3];
 };
 constexpr MxTile kMxTiles[kMxKinds] = {
-    {64, 64, 4, 4, 4, 2.56f, 1.36f, {0.218f, 0.279f, 0.64f}, {0.462f, 0.706f, 0.9f}},
-    {128, 128, 4, 4, 4, 1.77f, 3.46f, {0.471f, 0.653f, 1.42f}, {0.f, 0.f, 0.f}},
-    {256, 128, 2, 4, 4, 2.59f, 4.4f, {0.777f, 1.213f, 2.65f}, {0.f, 0.f, 0.f}},
+    {64, 64, 4, 4, 4, 2.56f, 1.36f, {0.218f, 0.279f, 0.656f}, {0.462f, 0.706f, 1.1f}},
+    {128, 128, 4, 4, 4, 1.77f, 3.46f, {0.471f, 0.653f, 1.287f}, {0.f, 0.f, 0.f}},
+    {256, 128, 2, 4, 4, 2.59f, 4.4f, {0.777f, 1.213f, 2.254f}, {0.f, 0.f, 0.f}},
     {256, 256, 2, 2, 8, 1.22f, 5.24f, {1.307f, 1.98f, 0.f}, {0.f, 0.f, 0.f}},
-    {16, 16, 1, 1, 4, 2.13f, 0.271f, {0.627f, 0.817f, 1.116f}, {0.067f, 0.064f, 0.119f}},
-    {32, 16, 1, 1, 4, 2.02f, 0.523f, {0.93f, 1.218f, 1.383f}, {0.122f, 0.056f, 0.191f}}};
+    {16, 16, 1, 1, 4, 2.13f, 0.271f, {0.627f, 0.817f, 1.044f}, {0.067f, 0.064f, 0.125f}},
+    {32, 16, 1, 1, 4, 2.02f, 0.523f, {0.93f, 1.218f, 1.338f}, {0.122f, 0.056f, 0.193f}}};
 // (fp32 sums of 8-bit rows' halves: the 256 x 256 tile's would not fit the registers)
 constexpr bool mx_kind_on(int kind, int bits, int dtype) { return kind != kMx256x256 || bits == 4 || dtype == LORA_BF16; }
+// Waves of a workgroup: 8-bit rows with fp32 y have two on a SIMD in the larger tiles
+// (launch_mx has the figures).
+constexpr int mx_waves(int kind, int bits, int dtype) {
+    return bits == 8 && dtype == LORA_F32 && (kind == kMx128x128 || kind == kMx256x128) ? 8 : kMxTiles[kind].waves;
+}
 
 // Estimated us of a call of `tiles` tiles (not counting parts of k), `steps` steps of 256
 // columns and s parts, after measurements of 1200 products and 800 experts' products of
 // random sizes (1 to 6783 rows, k 256 to 14336, 256 to 14336 outputs, each kernel and
 // split): on those that the numbers were not fitted to, the choice is 1.1% slower than the
-// best in the mean (experts' products, whose rows are spread as the router likes, 2.7%).
+// best in the mean (experts' products, whose rows are spread as the router likes, 2.7%;
+// fp32 y from 8-bit rows, by 260 and 200 sizes of its own, 0.5% and 1.4%).
 inline float mx_time(int kind, int bits, int dtype, int64_t tiles, int32_t steps, int32_t s, float outputs) {
     const MxTile& c = kMxTiles[kind];
     const int f = bits == 4 ? 0 : dtype == LORA_BF16 ? 1 : 2;
@@ -109,7 +116,7 @@ inline BasePlan mx_plan(int bits, int dtype, int64_t T, int64_t k, int64_t N) {
         for (const int32_t s : kSplits) {
             // (parts are of whole spans of scales, up to 1024 columns)
             if (s > 1 && (s > (steps + 3) / 4 || tiles * s > 2 * kCus || kind >= kMx16x16)) break;
-            if (!grid_fits(tiles * s + 8, c.waves * 64)) break;  // (rounded up to the XCDs)
+            if (!grid_fits(tiles * s + 8, mx_waves(kind, bits, dtype) * 64)) break;  // (rounded up to the XCDs)
             const float us = mx_time(kind, bits, dtype, tiles, steps, s, (float)T * (float)N);
             if (best.kind == kMxKinds || us < least) {
                 least = us;
@@ -132,7 +139,7 @@ inline BasePlan mx_expert_plan(int bits, int dtype, int64_t T, int64_t k, int64_
         if (!mx_kind_on(kind, bits, dtype)) continue;
         const MxTile& c = kMxTiles[kind];
         const int64_t most = T / c.bt + used, tiles_n = (N + c.bn - 1) / c.bn;
-        if (!grid_fits(most * tiles_n + 8, c.waves * 64)) continue;
+        if (!grid_fits(most * tiles_n + 8, mx_waves(kind, bits, dtype) * 64)) continue;
         const float each = std::max(1.f, (float)T / (float)(used * c.bt) + 0.5f);
         const float us = mx_time(kind, bits, dtype, (int64_t)((float)(tiles_n * used) * each), steps, 1, 0.f);
         if (best.kind == kMxKinds || us < least) {

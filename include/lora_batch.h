@@ -623,7 +623,8 @@ size_t lora_base_product_mx_workspace_bytes(int32_t T, int32_t d_in, int32_t d_o
  *          W_k = max(|w_k|, s) in its bound (0 for w_k = 0), s the scale of w_k's block.
  *   ws: lora_base_product_mx_workspace_bytes(T, d_in, d_out) bytes.
  * Rows are independent, and the order of every sum is fixed by the shapes, as in
- * lora_base_product, and so are its refusals (pitches of scales included).
+ * lora_base_product, and so are its refusals (pitches of scales included; LORA_F32
+ * with x_bits = 8: a launch's tiles hold 2^38 outputs).
  */
 int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
                          int64_t ldy, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);

@@ -87,7 +87,7 @@ int main() {
             continue;
         }
         const MxTile& c = kMxTiles[b.kind];
-        printf("%dx%d %d %d %zu %ld\\n", c.bn, c.bt, b.splits, c.waves, base_workspace_bytes(b, T, n), (long)tiles_t);
+        printf("%dx%d %d %d %zu %ld\\n", c.bn, c.bt, b.splits, mx_waves(b.kind, (int)bits, (int)dt), base_workspace_bytes(b, T, n), (long)tiles_t);
     }
     return 0;
 }
@@ -155,7 +155,8 @@ def test_products_of_very_many_rows_or_outputs_fit_a_launch(plan, lib):
                 got = lib.lora_base_product_mx(int(dt == "f32"), bits, x, T, k, w, n, FAKE, n, 0, FAKE, 2 ** 62, None)
             assert got == _abi.LORA_ERR_UNSUPPORTED
             held = T * n * (4 if dt == "f32" else 2) + (T * 132 + max(1, e) * n * 136) * -(-k // 256)
-            assert held > 288e9  # more than a GPU holds
+            many = bits == 8 and dt == "f32" and -(-n // 256) * -(-T // 128) >= 2 ** 23 - 8  # (tiles of 8 waves)
+            assert many or held > 288e9  # more than a GPU holds
 
 
 def test_weights_of_more_rows_than_a_launch_are_refused(lib):
