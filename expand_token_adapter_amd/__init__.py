@@ -924,9 +924,11 @@ def _expert_segments(fn: str, seg) -> None:
         raise ValueError("tensors must be on the GPU")
 
 
-def _same(fn: str, name: str, d: int, code: int, d0: int, code0: int) -> None:
+def _same(fn: str, name: str, d: int, code: int, d0: int, code0: int, p: int = 0, p0: int = -1) -> None:
     if d != d0 or code != code0:
         raise ValueError(f"{fn}: {name} must have {d0} columns of the same type")
+    if p and p == p0:  # (another token's row would be written before it is read)
+        raise ValueError(f"{fn}: {name} is the rows that are read")
 
 
 def _router_weights(fn: str, seg: ExpertSegments, w: torch.Tensor, name: str = "w") -> int:
@@ -944,7 +946,7 @@ def lora_expert_gather(x: torch.Tensor, seg: ExpertSegments, y: Optional[torch.T
     if y is None:
         y = torch.zeros(seg.T, d, dtype=x.dtype, device=x.device)
     py, dy, ldy, cy = _matrix(fn, y, "y", seg.T, seg.index)
-    _same(fn, "y", dy, cy, d, code)
+    _same(fn, "y", dy, cy, d, code, py, px)
     st = _launch_on(seg.index, _abi.load().lora_expert_gather, code, px, ldx, seg.tokens, d, seg.k, seg.pos.data_ptr(), py, ldy)
     if st:
         _abi.check(fn, st)
@@ -962,7 +964,7 @@ def lora_expert_gather_backward(dy: torch.Tensor, seg: ExpertSegments, dx: Optio
             raise ValueError(f"{fn}: accumulate needs dx")
         dx = torch.empty(seg.tokens, d, dtype=dy.dtype, device=dy.device)
     pdx, d2, lddx, c2 = _matrix(fn, dx, "dx", seg.tokens, seg.index)
-    _same(fn, "dx", d2, c2, d, code)
+    _same(fn, "dx", d2, c2, d, code, pdx, pdy)
     st = _launch_on(seg.index, _abi.load().lora_expert_gather_backward, code, pdy, lddy, seg.tokens, d, seg.k, seg.pos.data_ptr(),
                     pdx, lddx, 1 if accumulate else 0)
     if st:
@@ -983,7 +985,7 @@ def lora_expert_combine(o: torch.Tensor, w: torch.Tensor, seg: ExpertSegments, y
             raise ValueError(f"{fn}: accumulate needs y")
         y = torch.empty(seg.tokens, d, dtype=o.dtype, device=o.device)
     py, dy, ldy, cy = _matrix(fn, y, "y", seg.tokens, seg.index)
-    _same(fn, "y", dy, cy, d, code)
+    _same(fn, "y", dy, cy, d, code, py, po)
     st = _launch_on(seg.index, _abi.load().lora_expert_combine, code, po, ldo, seg.tokens, d, seg.k, seg.pos.data_ptr(), pw, py, ldy,
                     1 if accumulate else 0)
     if st:
@@ -1007,7 +1009,7 @@ def lora_expert_combine_backward(dy: torch.Tensor, o: torch.Tensor, w: torch.Ten
     if dw is None:
         dw = torch.empty(seg.tokens, seg.k, dtype=torch.float32, device=dy.device)
     pd, d2, ldd, c2 = _matrix(fn, d_o, "d_o", seg.T, seg.index)
-    _same(fn, "d_o", d2, c2, d, code)
+    _same(fn, "d_o", d2, c2, d, code, pd, pdy)
     st = _launch_on(seg.index, _abi.load().lora_expert_combine_backward, code, pdy, lddy, po, ldo, seg.tokens, d, seg.k,
                     seg.pos.data_ptr(), pw, pd, ldd, _router_weights(fn, seg, dw, "dw"))
     if st:

@@ -636,6 +636,7 @@ int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int
  * rows are by adapter; the rows that go through the experts lie sorted, expert e's
  * at seg.offsets[e] .. seg.offsets[e + 1] - 1.  Adapters of the sorted rows are
  * applied as of any rows (lora_segments_build over the sorted rows' adapter ids).
+ * No output of these calls shares memory with an input unless a call says so.
  */
 
 /*

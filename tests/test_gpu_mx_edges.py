@@ -172,3 +172,16 @@ def test_gradients_of_the_combine_for_many_tokens(T, k, d, dtype):
     rows = torch.nan_to_num(o.double())[at]
     exact, mag = (dy.double().unsqueeze(1) * rows).sum(-1), (dy.double().unsqueeze(1) * rows).abs().sum(-1)
     assert ((dw.double() - exact).abs()[on] <= (d / 64 + 16) * 2.0 ** -24 * mag[on]).all()
+
+
+def test_rows_are_not_sorted_or_joined_in_place():
+    """With one choice a token the rows there and back have one shape, but not one order."""
+    seg = lb.lora_expert_segments(torch.randint(0, 4, (30, 1), dtype=torch.int32, device="cuda"), 4)
+    x, w = torch.randn(30, 64, device="cuda"), torch.rand(30, 1, device="cuda")
+    for bad in (lambda: lb.lora_expert_gather(x, seg, y=x), lambda: lb.lora_expert_gather_backward(x, seg, dx=x),
+                lambda: lb.lora_expert_combine(x, w, seg, y=x),
+                lambda: lb.lora_expert_combine_backward(x, x.clone(), w, seg, d_o=x)):
+        with pytest.raises(ValueError):
+            bad()
+    empty = lb.lora_expert_segments(torch.zeros(0, 1, dtype=torch.int32, device="cuda"), 4)
+    assert lb.lora_expert_combine(x[:0], w[:0], empty).shape == (0, 64)
