@@ -33,14 +33,16 @@ int launch_mx(MxParams p, const BasePlan& b, int64_t tiles_t, hipStream_t st) {
     p.tiles_n = (p.N + c.bn - 1) / c.bn;
     p.tiles_t = (int32_t)tiles_t;
     const unsigned grid = (unsigned)round_up(p.tiles_n * tiles_t * p.splits, kNumXcd);
-    // Rows in halves: in the smallest tile no two waves share an activation row, whose codes
+    // Rows in halves: in the 64 x 64 tile no two waves share an activation row, whose codes
     // each would take apart (256 x 4096 x 4096 16.1 us in place of 18.7; in one piece 10.0
-    // against 9.7); the larger ones have two waves on a SIMD, one to take codes apart while
+    // against 9.7; in the 64 x 32 tile 317 x 5128 x 1032 14.1 with two that share, 15.1
+    // without); the larger ones have two waves on a SIMD, one to take codes apart while
     // the other multiplies (128 x 128 outputs x rows a tile: 256 x 4096 x 4096 30.3 -> 26.5 us,
     // 2048 x 14336 x 4096 204 -> 195; 256 x 128: 49.7 -> 44.2, 184 -> 175; in one piece
     // 119 -> 122, 103 -> 108).
     constexpr bool kHalves = kMxHalves<XB, DT>;
     switch (b.kind) {
+        case kMx64x32: launch_tiles<XB, DT, kMx64x32, 2, 2>(p, grid, st); break;
         case kMx64x64: launch_tiles<XB, DT, kMx64x64, kHalves ? 1 : 2, kHalves ? 4 : 2>(p, grid, st); break;
         case kMx128x128: launch_tiles<XB, DT, kMx128x128, 2, kHalves ? 4 : 2>(p, grid, st); break;
         case kMx256x128: launch_tiles<XB, DT, kMx256x128, 2, kHalves ? 4 : 2>(p, grid, st); break;

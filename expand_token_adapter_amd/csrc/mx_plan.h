@@ -3,17 +3,18 @@
 //
 // Measured (us, bf16 y, 4-bit / 8-bit rows; rows x k x outputs; the last two kernels read
 // the weight straight into registers):
-//                          64x64      128x128    256x128    256x256    16x16      32x16
-//     1 x  4096 x  4096  6.5/8.0                                      3.4/3.7    4.6/4.8
-//    16 x 14336 x  4096   16/21                                       9.7/12.8    13/16
-//    32 x  4096 x  4096  6.8/8.6                                      6.7/8.7    5.7/6.8
-//   256 x  4096 x  4096  8.0/10.8    13/16      19/26      28/40
-//  1024 x  4096 x  4096   22/30      16/19      20/27      29/41
-//  2048 x 14336 x  4096  121/189     77/104     64/89      88/120
-//  6783 x  4096 x 14336  487/631    354/409    278/347    223/294
-// (fp32 y from 8-bit rows, taken in two halves: 256 x 4096 x 4096 16.1 us with 64x64,
-// 2048 x 14336 x 4096 174 and
-// 6783 x 4096 x 14336 655 with 256x128.)
+//                          64x32      64x64     128x128    256x128    256x256    16x16      32x16
+//     1 x  4096 x  4096  5.4/6.9    6.4/7.9                                    3.4/3.7    4.6/4.8
+//    16 x 14336 x  4096   13/19      15/20                                     9.7/12.8    13/16
+//    32 x  4096 x  4096  5.6/7.2    6.6/8.2                                    6.7/8.7    5.7/6.8
+//   128 x  4096 x  4096  6.2/8.3    7.2/9.3
+//   256 x  4096 x  4096  9.1/13     7.9/9.8    13/16      19/26      28/40
+//  1024 x  4096 x  4096   31/41      22/29     16/19      20/27      29/41
+//  2048 x 14336 x  4096             121/189    77/104     64/89      88/120
+//  6783 x  4096 x 14336             487/631   354/409    278/347    223/294
+// (fp32 y from 8-bit rows, taken in two halves: 317 x 5128 x 1032 14.1 us with 64x32, 18 with
+// 64x64, 256 x 4096 x 4096 16.1 with 64x64, 2048 x 14336 x 4096 174 and 6783 x 4096 x 14336
+// 655 with 256x128.)
 #pragma once
 
 #include <stddef.h>
@@ -55,7 +56,7 @@ struct MxLds {
 };
 
 // Kernels: tiles through LDS, and (from kMx16x16 on) tiles of waves side by side along k.
-enum { kMx64x64 = 0, kMx128x128, kMx256x128, kMx256x256, kMx16x16, kMx32x16, kMxKinds };
+enum { kMx64x32 = 0, kMx64x64, kMx128x128, kMx256x128, kMx256x256, kMx16x16, kMx32x16, kMxKinds };
 struct MxTile {
     int32_t bn, bt;            // outputs, rows
     int32_t stages4, stages8;  // of the ring in LDS, for 4-bit and 8-bit rows
@@ -66,12 +67,13 @@ struct MxTile {
     float start, tile, step[3], shared[3];
 };
 constexpr MxTile kMxTiles[kMxKinds] = {
-    {64, 64, 4, 4, 4, 2.56f, 1.36f, {0.218f, 0.279f, 0.656f}, {0.462f, 0.706f, 1.1f}},
+    {64, 32, 4, 4, 4, 2.889f, 0.994f, {0.166f, 0.194f, 0.539f}, {0.453f, 0.332f, 0.746f}},
+    {64, 64, 4, 4, 4, 2.496f, 1.36f, {0.216f, 0.31f, 0.751f}, {0.493f, 0.666f, 0.998f}},
     {128, 128, 4, 4, 4, 1.77f, 3.46f, {0.471f, 0.653f, 1.287f}, {0.f, 0.f, 0.f}},
     {256, 128, 2, 4, 4, 2.59f, 4.4f, {0.777f, 1.213f, 2.254f}, {0.f, 0.f, 0.f}},
     {256, 256, 2, 2, 8, 1.22f, 5.24f, {1.307f, 1.98f, 0.f}, {0.f, 0.f, 0.f}},
-    {16, 16, 1, 1, 4, 2.13f, 0.271f, {0.627f, 0.817f, 1.044f}, {0.067f, 0.064f, 0.125f}},
-    {32, 16, 1, 1, 4, 2.02f, 0.523f, {0.93f, 1.218f, 1.338f}, {0.122f, 0.056f, 0.193f}}};
+    {16, 16, 1, 1, 4, 2.13f, 0.292f, {0.684f, 0.817f, 1.044f}, {0.071f, 0.071f, 0.118f}},
+    {32, 16, 1, 1, 4, 2.02f, 0.513f, {1.088f, 1.165f, 1.339f}, {0.134f, 0.068f, 0.193f}}};
 // (fp32 sums of 8-bit rows' halves: the 256 x 256 tile's would not fit the registers)
 constexpr bool mx_kind_on(int kind, int bits, int dtype) { return kind != kMx256x256 || bits == 4 || dtype == LORA_BF16; }
 // Waves of a workgroup: 8-bit rows with fp32 y have two on a SIMD in the larger tiles
@@ -83,9 +85,9 @@ constexpr int mx_waves(int kind, int bits, int dtype) {
 // Estimated us of a call of `tiles` tiles (not counting parts of k), `steps` steps of 256
 // columns and s parts, after measurements of 1200 products and 800 experts' products of
 // random sizes (1 to 6783 rows, k 256 to 14336, 256 to 14336 outputs, each kernel and
-// split): on those that the numbers were not fitted to, the choice is 1.1% slower than the
-// best in the mean (experts' products, whose rows are spread as the router likes, 2.7%;
-// fp32 y from 8-bit rows, by 260 and 200 sizes of its own, 0.5% and 1.4%).
+// split), and 900 and 500 more for the small kernels: on those that the numbers were not
+// fitted to, the choice is 0.9% slower than the best in the mean (experts' products, whose
+// rows are spread as the router likes, 2.6%; without the 64 x 32 tile 3.6% and 7.7%).
 inline float mx_time(int kind, int bits, int dtype, int64_t tiles, int32_t steps, int32_t s, float outputs) {
     const MxTile& c = kMxTiles[kind];
     const int f = bits == 4 ? 0 : dtype == LORA_BF16 ? 1 : 2;
@@ -94,7 +96,7 @@ inline float mx_time(int kind, int bits, int dtype, int64_t tiles, int32_t steps
     float us = c.start;
     if (kind >= kMx16x16) {
         us += (float)(((steps + 1) / 2 + c.waves - 1) / c.waves) * c.step[f] + (float)n / kCus * (c.tile + st * c.shared[f]);
-    } else if (kind == kMx64x64) {  // two on a CU
+    } else if (kind <= kMx64x64) {  // two on a CU, or more
         const int64_t full = n / (2 * kCus), rest = n - full * 2 * kCus;
         us += (float)full * (c.tile + st * c.shared[f]);
         if (rest > 0) us += c.tile + st * (rest <= kCus ? c.step[f] : c.shared[f]);

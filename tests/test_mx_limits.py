@@ -76,7 +76,7 @@ constexpr bool lds() {
     constexpr MxTile c = kMxTiles[K];
     return MxLds<c.bn, c.bt, c.stages4, 4>::kBytes <= kLdsBytes && MxLds<c.bn, c.bt, c.stages8, 8>::kBytes <= kLdsBytes;
 }
-static_assert(lds<kMx64x64>() && lds<kMx128x128>() && lds<kMx256x128>() && lds<kMx256x256>(), "a CU's LDS");
+static_assert(lds<kMx64x32>() && lds<kMx64x64>() && lds<kMx128x128>() && lds<kMx256x128>() && lds<kMx256x256>(), "a CU's LDS");
 int main() {
     long bits, dt, T, k, n, e;
     while (scanf("%ld %ld %ld %ld %ld %ld", &bits, &dt, &T, &k, &n, &e) == 6) {
