@@ -67,13 +67,13 @@ struct MxTile {
     float start, tile, step[3], shared[3];
 };
 constexpr MxTile kMxTiles[kMxKinds] = {
-    {64, 32, 4, 4, 4, 2.889f, 0.994f, {0.166f, 0.194f, 0.539f}, {0.453f, 0.332f, 0.746f}},
-    {64, 64, 4, 4, 4, 2.496f, 1.36f, {0.216f, 0.31f, 0.751f}, {0.493f, 0.666f, 0.998f}},
+    {64, 32, 4, 4, 4, 2.891f, 0.978f, {0.158f, 0.241f, 0.476f}, {0.437f, 0.402f, 0.746f}},
+    {64, 64, 4, 4, 4, 2.496f, 1.365f, {0.217f, 0.315f, 0.749f}, {0.49f, 0.784f, 0.985f}},
     {128, 128, 4, 4, 4, 1.77f, 3.46f, {0.471f, 0.653f, 1.287f}, {0.f, 0.f, 0.f}},
     {256, 128, 2, 4, 4, 2.59f, 4.4f, {0.777f, 1.213f, 2.254f}, {0.f, 0.f, 0.f}},
     {256, 256, 2, 2, 8, 1.22f, 5.24f, {1.307f, 1.98f, 0.f}, {0.f, 0.f, 0.f}},
-    {16, 16, 1, 1, 4, 2.13f, 0.292f, {0.684f, 0.817f, 1.044f}, {0.071f, 0.071f, 0.118f}},
-    {32, 16, 1, 1, 4, 2.02f, 0.513f, {1.088f, 1.165f, 1.339f}, {0.134f, 0.068f, 0.193f}}};
+    {16, 16, 1, 1, 4, 2.312f, 0.278f, {0.639f, 0.545f, 0.991f}, {0.092f, 0.13f, 0.16f}},
+    {32, 16, 1, 1, 4, 1.812f, 0.829f, {0.774f, 1.005f, 1.403f}, {0.156f, 0.182f, 0.223f}}};
 // (fp32 sums of 8-bit rows' halves: the 256 x 256 tile's would not fit the registers)
 constexpr bool mx_kind_on(int kind, int bits, int dtype) { return kind != kMx256x256 || bits == 4 || dtype == LORA_BF16; }
 // Waves of a workgroup: 8-bit rows with fp32 y have two on a SIMD in the larger tiles
@@ -85,9 +85,10 @@ constexpr int mx_waves(int kind, int bits, int dtype) {
 // Estimated us of a call of `tiles` tiles (not counting parts of k), `steps` steps of 256
 // columns and s parts, after measurements of 1200 products and 800 experts' products of
 // random sizes (1 to 6783 rows, k 256 to 14336, 256 to 14336 outputs, each kernel and
-// split), and 900 and 500 more for the small kernels: on those that the numbers were not
-// fitted to, the choice is 0.9% slower than the best in the mean (experts' products, whose
-// rows are spread as the router likes, 2.6%; without the 64 x 32 tile 3.6% and 7.7%).
+// split), and for the small kernels 900 and 500 more and 400 products of up to 64 rows: on
+// those that the numbers were not fitted to, the choice is 0.4% slower than the best in the
+// mean (few rows 0.6%; experts' products, whose rows are spread as the router likes, 2.4%;
+// without the 64 x 32 tile 3.6% and experts' 7.7%).
 inline float mx_time(int kind, int bits, int dtype, int64_t tiles, int32_t steps, int32_t s, float outputs) {
     const MxTile& c = kMxTiles[kind];
     const int f = bits == 4 ? 0 : dtype == LORA_BF16 ? 1 : 2;
@@ -95,7 +96,9 @@ inline float mx_time(int kind, int bits, int dtype, int64_t tiles, int32_t steps
     const float st = (float)(s == 1 ? steps : 4 * (((steps + 3) / 4 + s - 1) / s));
     float us = c.start;
     if (kind >= kMx16x16) {
-        us += (float)(((steps + 1) / 2 + c.waves - 1) / c.waves) * c.step[f] + (float)n / kCus * (c.tile + st * c.shared[f]);
+        // (one workgroup's way through its k, or that of all that a CU has)
+        const float alone = (float)(((steps + 1) / 2 + c.waves - 1) / c.waves) * c.step[f] + c.tile;
+        us += std::max(alone, (float)((n + kCus - 1) / kCus) * (c.tile + st * c.shared[f]));
     } else if (kind <= kMx64x64) {  // two on a CU, or more
         const int64_t full = n / (2 * kCus), rest = n - full * 2 * kCus;
         us += (float)full * (c.tile + st * c.shared[f]);
