@@ -858,7 +858,7 @@ def lora_base_product_mx_workspace_bytes(T: int, d_in: int, d_out: int) -> int:
     return _abi.load().lora_base_product_mx_workspace_bytes(T, d_in, d_out)
 
 
-def _mx_operands(fn: str, x, w, y, accumulate: bool, dtype, new):
+def _mx_operands(fn: str, x, w, y, accumulate: bool, dtype, cut: bool, new):
     """Checked (x_bits, y, its pointer, pitch and type code) of a product of rows x (MxRows or QuantRows) and a 4-bit weight w."""
     bits = 4 if isinstance(x, MxRows) else 8 if isinstance(x, QuantRows) else 0
     if not bits or not isinstance(w, MxWeight):
@@ -872,18 +872,23 @@ def _mx_operands(fn: str, x, w, y, accumulate: bool, dtype, new):
     py, d_out, ldy, code = _matrix(fn, y, "y", x.T, w.index)
     if d_out != w.d_out:
         raise ValueError(f"{fn}: y must be [{x.T}, {w.d_out}]")
+    if cut:
+        if bits != 8 or code != LORA_BF16:
+            raise ValueError(f"{fn}: products are cut of 8-bit rows with bfloat16 y alone")
+        bits |= _abi.LORA_MX_CUT
     return bits, y, py, ldy, code
 
 
 def lora_base_product_mx(x, w: MxWeight, y: Optional[torch.Tensor] = None, accumulate: bool = False,
-                         dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+                         dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None,
+                         cut: bool = False) -> torch.Tensor:
     """y = W x for every row (accumulate: y += W x) with a 4-bit weight; x: MxRows (4 bits) or QuantRows (8 bits);
     without y, a new tensor [T, d_out] of dtype.
 
-    Sums are fp32, rounded once.  Products are exact but for 8-bit rows with bfloat16 y, where the matrix instruction
-    cuts them as in lora_base_product."""
+    Sums are fp32 of exact products, rounded once.  cut, for 8-bit rows with bfloat16 y: the matrix instruction may cut
+    the products, as in lora_base_product, for half of the work of a large product."""
     fn = "lora_base_product_mx"
-    bits, y, py, ldy, code = _mx_operands(fn, x, w, y, accumulate, dtype, torch.empty)
+    bits, y, py, ldy, code = _mx_operands(fn, x, w, y, accumulate, dtype, cut, torch.empty)
     if w.experts is not None:
         raise ValueError(f"{fn}: w holds several experts' weights (lora_expert_product_mx)")
     lib = _abi.load()
@@ -1018,14 +1023,14 @@ def lora_expert_combine_backward(dy: torch.Tensor, o: torch.Tensor, w: torch.Ten
 
 
 def lora_expert_product_mx(x, w: MxWeight, seg: Segments, y: Optional[torch.Tensor] = None, accumulate: bool = False,
-                           dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+                           dtype: torch.dtype = torch.bfloat16, cut: bool = False) -> torch.Tensor:
     """y[i] = W_e x[i] (accumulate: +=) for every sorted row i of expert e, each expert with its own 4-bit weight, in
     one launch.  x: MxRows or QuantRows of the sorted rows; w: MxWeight with experts.  Rows behind the last expert's
-    are left as they are (zeros in a new y).  Precision: as lora_base_product_mx."""
+    are left as they are (zeros in a new y).  Precision, and cut: as lora_base_product_mx."""
     fn = "lora_expert_product_mx"
     if not isinstance(seg, Segments):
         raise TypeError(f"{fn}: seg must be a Segments (lora_expert_segments)")
-    bits, y, py, ldy, code = _mx_operands(fn, x, w, y, accumulate, dtype, torch.zeros)
+    bits, y, py, ldy, code = _mx_operands(fn, x, w, y, accumulate, dtype, cut, torch.zeros)
     experts = w.experts or 1
     if seg.T != x.T or seg.num_adapters != experts or seg.offsets.get_device() != w.index:
         raise ValueError(f"{fn}: the segments are of {seg.T} rows and {seg.num_adapters} experts on {seg.offsets.device}, the call "

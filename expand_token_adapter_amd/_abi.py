@@ -69,6 +69,7 @@ LORA_QUANT_BLOCK = 128
 LORA_BASE_PRODUCT_MAX_WORKSPACE = 128 << 20
 LORA_MX_BLOCK = 32
 LORA_MX_PAD = 256
+LORA_MX_CUT = 256
 
 
 class LoraQuant(ctypes.Structure):

@@ -11,22 +11,22 @@ using namespace lora;
 namespace {
 
 // WN x WT waves a workgroup
-template <int XB, int DT, int KIND, int WN, int WT>
+template <int XB, int DT, bool HALVES, int KIND, int WN, int WT>
 void launch_tiles(const MxParams& p, unsigned grid, hipStream_t st) {
     constexpr MxTile c = kMxTiles[KIND];
-    static_assert(WN * WT == mx_waves(KIND, XB, DT), "the plan's bound on the launch");
-    hipLaunchKernelGGL((mx_kernel<c.bn, c.bt, WN, WT, XB == 4 ? c.stages4 : c.stages8, XB, DT>), dim3(grid), dim3(WN * WT * kWave), 0,
-                       st, p);
+    static_assert(WN * WT == mx_waves(KIND, XB, mx_sums(XB, DT, !HALVES)), "the plan's bound on the launch");
+    hipLaunchKernelGGL((mx_kernel<c.bn, c.bt, WN, WT, XB == 4 ? c.stages4 : c.stages8, XB, DT, HALVES>), dim3(grid),
+                       dim3(WN * WT * kWave), 0, st, p);
 }
-template <int XB, int DT, int KIND>
+template <int XB, int DT, bool HALVES, int KIND>
 void launch_stream(const MxParams& p, unsigned grid, hipStream_t st) {
     constexpr MxTile c = kMxTiles[KIND];
-    hipLaunchKernelGGL((mx_stream_kernel<c.waves, c.bn / 16, c.bt / 16, XB, DT>), dim3(grid),
+    hipLaunchKernelGGL((mx_stream_kernel<c.waves, c.bn / 16, c.bt / 16, XB, DT, HALVES>), dim3(grid),
                        dim3(c.waves * kWave), 0, st, p);
 }
 
 // tiles_t: tiles along t of all weights, at most
-template <int XB, int DT>
+template <int XB, int DT, bool HALVES>
 int launch_mx(MxParams p, const BasePlan& b, int64_t tiles_t, hipStream_t st) {
     p.splits = b.splits;
     const MxTile& c = kMxTiles[b.kind];
@@ -40,17 +40,16 @@ int launch_mx(MxParams p, const BasePlan& b, int64_t tiles_t, hipStream_t st) {
     // the other multiplies (128 x 128 outputs x rows a tile: 256 x 4096 x 4096 30.3 -> 26.5 us,
     // 2048 x 14336 x 4096 204 -> 195; 256 x 128: 49.7 -> 44.2, 184 -> 175; in one piece
     // 119 -> 122, 103 -> 108).
-    constexpr bool kHalves = kMxHalves<XB, DT>;
     switch (b.kind) {
-        case kMx64x32: launch_tiles<XB, DT, kMx64x32, 2, 2>(p, grid, st); break;
-        case kMx64x64: launch_tiles<XB, DT, kMx64x64, kHalves ? 1 : 2, kHalves ? 4 : 2>(p, grid, st); break;
-        case kMx128x128: launch_tiles<XB, DT, kMx128x128, 2, kHalves ? 4 : 2>(p, grid, st); break;
-        case kMx256x128: launch_tiles<XB, DT, kMx256x128, 2, kHalves ? 4 : 2>(p, grid, st); break;
+        case kMx64x32: launch_tiles<XB, DT, HALVES, kMx64x32, 2, 2>(p, grid, st); break;
+        case kMx64x64: launch_tiles<XB, DT, HALVES, kMx64x64, HALVES ? 1 : 2, HALVES ? 4 : 2>(p, grid, st); break;
+        case kMx128x128: launch_tiles<XB, DT, HALVES, kMx128x128, 2, HALVES ? 4 : 2>(p, grid, st); break;
+        case kMx256x128: launch_tiles<XB, DT, HALVES, kMx256x128, 2, HALVES ? 4 : 2>(p, grid, st); break;
         case kMx256x256:
-            if constexpr (mx_kind_on(kMx256x256, XB, DT)) launch_tiles<XB, DT, kMx256x256, 2, 4>(p, grid, st);
+            if constexpr (mx_kind_on(kMx256x256, XB, mx_sums(XB, DT, !HALVES))) launch_tiles<XB, DT, HALVES, kMx256x256, 2, 4>(p, grid, st);
             break;
-        case kMx16x16: launch_stream<XB, DT, kMx16x16>(p, grid, st); break;
-        default: launch_stream<XB, DT, kMx32x16>(p, grid, st); break;
+        case kMx16x16: launch_stream<XB, DT, HALVES, kMx16x16>(p, grid, st); break;
+        default: launch_stream<XB, DT, HALVES, kMx32x16>(p, grid, st); break;
     }
     if (hipGetLastError() != hipSuccess) return LORA_ERR_HIP;
     if (p.splits > 1) {
@@ -69,10 +68,19 @@ int launch_mx(MxParams p, const BasePlan& b, int64_t tiles_t, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
-int launch(const MxParams& p, int bits, int dtype, const BasePlan& b, int64_t tiles_t, void* stream) {
+// The rows of a call: their bits, and whether products of 8-bit rows may be cut.
+struct MxRowsArg {
+    int bits;
+    bool cut;
+};
+MxRowsArg rows_arg(int32_t x_bits) { return MxRowsArg{x_bits & ~LORA_MX_CUT, (x_bits & LORA_MX_CUT) != 0}; }
+
+int launch(const MxParams& p, MxRowsArg x, int dtype, const BasePlan& b, int64_t tiles_t, void* stream) {
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (bits == 4) return dtype == LORA_BF16 ? launch_mx<4, LORA_BF16>(p, b, tiles_t, st) : launch_mx<4, LORA_F32>(p, b, tiles_t, st);
-    return dtype == LORA_BF16 ? launch_mx<8, LORA_BF16>(p, b, tiles_t, st) : launch_mx<8, LORA_F32>(p, b, tiles_t, st);
+    if (x.bits == 4)
+        return dtype == LORA_BF16 ? launch_mx<4, LORA_BF16, false>(p, b, tiles_t, st) : launch_mx<4, LORA_F32, false>(p, b, tiles_t, st);
+    if (x.cut) return launch_mx<8, LORA_BF16, false>(p, b, tiles_t, st);
+    return dtype == LORA_BF16 ? launch_mx<8, LORA_BF16, true>(p, b, tiles_t, st) : launch_mx<8, LORA_F32, true>(p, b, tiles_t, st);
 }
 
 // What both products check; d_out: of one weight.
@@ -88,8 +96,8 @@ int check_product(int dtype, int32_t bits, const lora_quant& x, int32_t T, int32
         return LORA_ERR_UNSUPPORTED;
     return LORA_OK;
 }
-bool valid_product(int dtype, int32_t bits, int32_t T, int32_t d_in, int32_t d_out, int32_t accumulate) {
-    return valid_dtype(dtype) && (bits == 4 || bits == 8) && T >= 0 && d_in >= 1 && d_out >= 1 && (accumulate == 0 || accumulate == 1);
+bool valid_product(int dtype, MxRowsArg x, int32_t T, int32_t d_in, int32_t d_out, int32_t accumulate) {
+    return valid_dtype(dtype) && (x.bits == 4 || x.bits == 8) && (!x.cut || (x.bits == 8 && dtype == LORA_BF16)) && T >= 0 && d_in >= 1 && d_out >= 1 && (accumulate == 0 || accumulate == 1);
 }
 MxParams product_params(int32_t bits, const lora_quant& x, int32_t T, int32_t d_in, const lora_quant& w, int32_t d_out, void* y,
                         int64_t ldy, int32_t accumulate) {
@@ -125,30 +133,32 @@ extern "C" size_t lora_base_product_mx_workspace_bytes(int32_t T, int32_t d_in, 
 
 extern "C" int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
                                     int64_t ldy, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
-    if (!valid_product(dtype, x_bits, T, d_in, d_out, accumulate)) return LORA_ERR_INVALID_ARG;
+    const MxRowsArg xa = rows_arg(x_bits);
+    if (!valid_product(dtype, xa, T, d_in, d_out, accumulate)) return LORA_ERR_INVALID_ARG;
     if (T == 0) return LORA_OK;
-    const int rc = check_product(dtype, x_bits, x, T, d_in, w, d_out, y, ldy);
+    const int rc = check_product(dtype, xa.bits, x, T, d_in, w, d_out, y, ldy);
     if (rc != LORA_OK) return rc;
-    const BasePlan b = mx_plan(x_bits, dtype, T, d_in, d_out);
+    const BasePlan b = mx_plan(xa.bits, mx_sums(xa.bits, dtype, xa.cut), T, d_in, d_out);
     if (b.kind == kMxKinds) return LORA_ERR_UNSUPPORTED;
     if (!ws || !aligned16(ws) || ws_bytes < base_workspace_bytes(b, T, d_out)) return LORA_ERR_WORKSPACE;
-    MxParams p = product_params(x_bits, x, T, d_in, w, d_out, y, ldy, accumulate);
+    MxParams p = product_params(xa.bits, x, T, d_in, w, d_out, y, ldy, accumulate);
     p.part = static_cast<float*>(ws);
-    return launch(p, x_bits, dtype, b, (T + kMxTiles[b.kind].bt - 1) / kMxTiles[b.kind].bt, stream);
+    return launch(p, xa, dtype, b, (T + kMxTiles[b.kind].bt - 1) / kMxTiles[b.kind].bt, stream);
 }
 
 extern "C" int lora_expert_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t num_experts,
                                       int32_t d_out, lora_segments seg, void* y, int64_t ldy, int32_t accumulate, void* stream) {
-    if (!valid_product(dtype, x_bits, T, d_in, d_out, accumulate) || num_experts < 1) return LORA_ERR_INVALID_ARG;
+    const MxRowsArg xa = rows_arg(x_bits);
+    if (!valid_product(dtype, xa, T, d_in, d_out, accumulate) || num_experts < 1) return LORA_ERR_INVALID_ARG;
     if (T == 0) return LORA_OK;
     if (!seg.offsets) return LORA_ERR_INVALID_ARG;
-    const int rc = check_product(dtype, x_bits, x, T, d_in, w, d_out, y, ldy);
+    const int rc = check_product(dtype, xa.bits, x, T, d_in, w, d_out, y, ldy);
     if (rc != LORA_OK) return rc;
     int64_t tiles_t = 0;
-    const BasePlan b = mx_expert_plan(x_bits, dtype, T, d_in, d_out, num_experts, &tiles_t);
+    const BasePlan b = mx_expert_plan(xa.bits, mx_sums(xa.bits, dtype, xa.cut), T, d_in, d_out, num_experts, &tiles_t);
     if (b.kind == kMxKinds) return LORA_ERR_UNSUPPORTED;
-    MxParams p = product_params(x_bits, x, T, d_in, w, d_out, y, ldy, accumulate);
+    MxParams p = product_params(xa.bits, x, T, d_in, w, d_out, y, ldy, accumulate);
     p.offsets = seg.offsets;
     p.experts = num_experts;
-    return launch(p, x_bits, dtype, b, tiles_t, stream);
+    return launch(p, xa, dtype, b, tiles_t, stream);
 }

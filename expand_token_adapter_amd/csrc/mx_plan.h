@@ -1,7 +1,7 @@
 // mx_plan.h -- which kernel, tile and split of k a product with a 4-bit weight takes,
 // and the LDS of a tile (host and device, no HIP).
 //
-// Measured (us, bf16 y, 4-bit / 8-bit rows; rows x k x outputs; the last two kernels read
+// Measured (us, bf16 y, 4-bit rows / 8-bit rows with products cut; rows x k x outputs; the last two kernels read
 // the weight straight into registers):
 //                          64x32      64x64     128x128    256x128    256x256    16x16      32x16
 //     1 x  4096 x  4096  5.4/6.9    6.4/7.9                                    3.4/3.7    4.6/4.8
@@ -12,7 +12,7 @@
 //  1024 x  4096 x  4096   31/41      22/29     16/19      20/27      29/41
 //  2048 x 14336 x  4096             121/189    77/104     64/89      88/120
 //  6783 x  4096 x 14336             487/631   354/409    278/347    223/294
-// (fp32 y from 8-bit rows, taken in two halves: 317 x 5128 x 1032 14.1 us with 64x32, 18 with
+// (8-bit rows in two halves, fp32 y: 317 x 5128 x 1032 14.1 us with 64x32, 18 with
 // 64x64, 256 x 4096 x 4096 16.1 with 64x64, 2048 x 14336 x 4096 174 and 6783 x 4096 x 14336
 // 655 with 256x128.)
 #pragma once
@@ -62,7 +62,7 @@ struct MxTile {
     int32_t stages4, stages8;  // of the ring in LDS, for 4-bit and 8-bit rows
     int32_t waves;             // of a workgroup (mx_waves)
     // us: a call's start and end, a workgroup's; a step of 256 columns (a piece of 512 of
-    // every wave) for 4-bit rows, 8-bit rows with bf16 y, with fp32 y; a step where several
+    // every wave) for 4-bit rows, 8-bit rows with products cut, in halves; a step where several
     // workgroups share the CU (of all of them, or of each for the last two kernels)
     float start, tile, step[3], shared[3];
 };
@@ -74,9 +74,13 @@ constexpr MxTile kMxTiles[kMxKinds] = {
     {256, 256, 2, 2, 8, 1.22f, 5.24f, {1.307f, 1.98f, 0.f}, {0.f, 0.f, 0.f}},
     {16, 16, 1, 1, 4, 2.312f, 0.278f, {0.639f, 0.545f, 0.991f}, {0.092f, 0.13f, 0.16f}},
     {32, 16, 1, 1, 4, 1.812f, 0.829f, {0.774f, 1.005f, 1.403f}, {0.156f, 0.182f, 0.223f}}};
-// (fp32 sums of 8-bit rows' halves: the 256 x 256 tile's would not fit the registers)
+// (8-bit rows in halves: the 256 x 256 tile's would not fit the registers)
 constexpr bool mx_kind_on(int kind, int bits, int dtype) { return kind != kMx256x256 || bits == 4 || dtype == LORA_BF16; }
-// Waves of a workgroup: 8-bit rows with fp32 y have two on a SIMD in the larger tiles
+// What a choice goes by beside the rows' bits, `dtype` below: the type of y, for 8-bit rows
+// that of a call that sums as this one does: LORA_F32 with the codes in halves, LORA_BF16
+// with products that may be cut.
+constexpr int mx_sums(int bits, int dtype, bool cut) { return bits == 4 ? dtype : cut ? LORA_BF16 : LORA_F32; }
+// Waves of a workgroup: 8-bit rows in halves have two on a SIMD in the larger tiles
 // (launch_mx has the figures).
 constexpr int mx_waves(int kind, int bits, int dtype) {
     return bits == 8 && dtype == LORA_F32 && (kind == kMx128x128 || kind == kMx256x128) ? 8 : kMxTiles[kind].waves;

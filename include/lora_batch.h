@@ -616,16 +616,19 @@ size_t lora_base_product_mx_workspace_bytes(int32_t T, int32_t d_in, int32_t d_o
  *   x: rows [T, d_in] in the mx form (x_bits = 4) or in the 8-bit form of
  *   lora_quant_rows (x_bits = 8); w: mx form of the weight [d_out, d_in]; y [T, ldy]
  *   (dtype).  The sums (and y_t before, if added to) are fp32 and rounded once to y's
- *   type.  What they sum:
- *   LORA_F32, and LORA_BF16 with x_bits = 4: exact products.
- *   LORA_BF16 with x_bits = 8: products cut as in lora_base_product, each of the 8 of
- *          columns 8 i .. 8 i + 7 below 2^-13 of the power of two of the largest, with
- *          W_k = max(|w_k|, s) in its bound (0 for w_k = 0), s the scale of w_k's block.
+ *   type.  Products are exact, unless the caller allows them to be cut:
+ *   x_bits = 8 | LORA_MX_CUT (LORA_BF16 alone) makes each product of 8-bit rows once in
+ *   place of twice and cuts it as lora_base_product does, each of the 8 of columns
+ *   8 i .. 8 i + 7 below 2^-13 of the power of two of the largest, with
+ *   W_k = max(|w_k|, s) in its bound (0 for w_k = 0), s the scale of w_k's block.  On
+ *   ordinary rows that is a hundredth of y's rounding; where large products of different
+ *   groups cancel it can be more than y.
  *   ws: lora_base_product_mx_workspace_bytes(T, d_in, d_out) bytes.
  * Rows are independent, and the order of every sum is fixed by the shapes, as in
- * lora_base_product, and so are its refusals (pitches of scales included; LORA_F32
- * with x_bits = 8: a launch's tiles hold 2^38 outputs).
+ * lora_base_product, and so are its refusals (pitches of scales included; 8-bit rows
+ * whose products are not cut: a launch's tiles hold 2^38 outputs).
  */
+#define LORA_MX_CUT 256 /* or-ed to x_bits = 8: products of 8-bit rows may be cut (LORA_BF16) */
 int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int32_t d_in, lora_quant w, int32_t d_out, void* y,
                          int64_t ldy, int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
 
