@@ -203,6 +203,13 @@ int check_expert(int dtype, int32_t T, int32_t d, int32_t k, const int32_t* pos)
 }
 bool valid_f32(const float* p) { return p && ((uintptr_t)p & 3u) == 0; }
 
+// Rows of d values, and an array of 4-byte numbers of the choices.
+RowSpan rows_span(int dtype, const void* p, int64_t rows, int32_t d, int64_t ld) {
+    const int64_t eb = dtype == LORA_BF16 ? 2 : 4;
+    return RowSpan::matrix(p, rows, d * eb, ld, eb);
+}
+RowSpan choices_span(const void* p, int32_t T, int32_t k) { return RowSpan::array(p, (int64_t)T * k * 4); }
+
 // Workgroups for 8 columns a thread.
 int64_t columns_grid(int32_t T, int32_t d) { return ((int64_t)T * (d / 8) + kThreads - 1) / kThreads; }
 
@@ -235,6 +242,8 @@ extern "C" int lora_expert_gather(int dtype, const void* x, int64_t ldx, int32_t
     if (rc == LORA_OK) rc = check_matrix(y, d, ldy);
     if (rc != LORA_OK) return rc;
     if (!grid_fits(columns_grid(T, d), kThreads)) return LORA_ERR_UNSUPPORTED;
+    const RowSpan out = rows_span(dtype, y, (int64_t)T * k, d, ldy);
+    if (shares_memory(out, rows_span(dtype, x, T, d, ldx)) || shares_memory(out, choices_span(pos, T, k))) return LORA_ERR_INVALID_ARG;
     ExpertParams p{};
     p.x = static_cast<const char*>(x);
     p.ldx = ldx;
@@ -264,6 +273,10 @@ int combine(int dtype, const void* o, int64_t ldo, int32_t T, int32_t d, int32_t
     if (rc == LORA_OK) rc = check_matrix(y, d, ldy);
     if (rc != LORA_OK) return rc;
     if (!grid_fits(columns_grid(T, d), kThreads)) return LORA_ERR_UNSUPPORTED;
+    const RowSpan out = rows_span(dtype, y, T, d, ldy);
+    if (shares_memory(out, rows_span(dtype, o, (int64_t)T * k, d, ldo)) || shares_memory(out, choices_span(pos, T, k)) ||
+        (weighted && shares_memory(out, choices_span(w, T, k))))
+        return LORA_ERR_INVALID_ARG;
     ExpertParams p{};
     p.o = static_cast<const char*>(o);
     p.ldo = ldo;
@@ -301,6 +314,16 @@ extern "C" int lora_expert_combine_backward(int dtype, const void* dy, int64_t l
     if (rc == LORA_OK && d_o) rc = check_matrix(d_o, d, lddo);
     if (rc != LORA_OK) return rc;
     if (!grid_fits(T, kThreads)) return LORA_ERR_UNSUPPORTED;
+    const RowSpan in_dy = rows_span(dtype, dy, T, d, lddy), in_o = rows_span(dtype, o, (int64_t)T * k, d, ldo);
+    const RowSpan in_w = choices_span(w, T, k), in_pos = choices_span(pos, T, k);
+    const RowSpan out_o = rows_span(dtype, d_o, (int64_t)T * k, d, lddo), out_w = choices_span(dw, T, k);
+    // (rows in place are read before they are written, if they are the same rows)
+    const bool in_place = d_o == o && lddo == ldo;
+    if (d_o && (shares_memory(out_o, in_dy) || shares_memory(out_o, in_w) || shares_memory(out_o, in_pos) ||
+                (dw && !in_place && shares_memory(out_o, in_o)) || (dw && shares_memory(out_o, out_w))))
+        return LORA_ERR_INVALID_ARG;
+    if (dw && (shares_memory(out_w, in_dy) || shares_memory(out_w, in_o) || shares_memory(out_w, in_w) || shares_memory(out_w, in_pos)))
+        return LORA_ERR_INVALID_ARG;
     ExpertParams p{};
     p.x = static_cast<const char*>(dy);
     p.ldx = lddy;

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "lora_batch.h"
 
 namespace lora {
@@ -20,6 +22,40 @@ inline int check_matrix(const void* p, int64_t cols, int64_t ld) {
     if (!aligned16(p)) return LORA_ERR_INVALID_ARG;
     if (cols % 8 != 0 || ld % 8 != 0) return LORA_ERR_UNSUPPORTED;
     return LORA_OK;
+}
+
+// Memory that an argument takes: `rows` rows of `bytes` bytes, `pitch` bytes from one to
+// the next.  (128-bit sums: a pitch is any number of the caller's.)
+struct RowSpan {
+    uintptr_t at;
+    int64_t rows, bytes;
+    __int128 pitch;
+    __int128 begin(int64_t i) const { return (__int128)at + i * pitch; }
+    __int128 end() const { return begin(rows - 1) + bytes; }
+    static RowSpan matrix(const void* p, int64_t rows, int64_t row_bytes, int64_t ld, int64_t unit) {
+        return RowSpan{(uintptr_t)p, rows, row_bytes, (__int128)ld * unit};
+    }
+    static RowSpan array(const void* p, int64_t bytes) { return RowSpan{(uintptr_t)p, 1, bytes, bytes}; }
+};
+// Whether two arguments share a byte.  Rows of one may lie between those of the other
+// (columns of one wider matrix): that is not sharing.
+inline bool shares_memory(const RowSpan& a, const RowSpan& b) {
+    if (a.rows > b.rows) return shares_memory(b, a);
+    if (a.rows < 1 || a.end() <= (__int128)b.at || b.end() <= (__int128)a.at) return false;
+    const __int128 d = (__int128)b.at - (__int128)a.at;
+    if (a.pitch == b.pitch) {
+        // row i of a meets row j of b where (i - j) pitch lies above d - a.bytes and below
+        // d + b.bytes: the first i - j above, from 1 - b.rows on
+        const __int128 low = d - a.bytes, p = a.pitch;
+        const __int128 m = std::max<__int128>((low < 0 ? -((p - 1 - low) / p) : low / p) + 1, 1 - b.rows);
+        return m < a.rows && m * p < d + b.bytes;
+    }
+    for (int64_t i = 0; i < a.rows; ++i) {  // the first row of b that ends behind a row's begin: does it begin before its end?
+        const __int128 low = i * a.pitch - b.bytes - d;
+        const __int128 j = low < 0 ? 0 : low / b.pitch + 1;
+        if (j < b.rows && d + j * b.pitch < i * a.pitch + a.bytes) return true;
+    }
+    return false;
 }
 
 inline int check_common(int dtype, int32_t T, int32_t num_adapters, int32_t r_max, const lora_adapter* adapters,

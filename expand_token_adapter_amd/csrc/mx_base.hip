@@ -157,6 +157,15 @@ extern "C" int lora_expert_product_mx(int dtype, int32_t x_bits, lora_quant x, i
     int64_t tiles_t = 0;
     const BasePlan b = mx_expert_plan(xa.bits, mx_sums(xa.bits, dtype, xa.cut), T, d_in, d_out, num_experts, &tiles_t);
     if (b.kind == kMxKinds) return LORA_ERR_UNSUPPORTED;
+    const int64_t eb = dtype == LORA_BF16 ? 2 : 4, rows_w = (int64_t)num_experts * d_out;
+    const int64_t col_x = xa.bits == 4 ? round_up(d_in, kMxPad) / 2 : round_up(d_in, kQBlock), col_w = round_up(d_in, kMxPad) / 2;
+    const int64_t col_xs = xa.bits == 4 ? round_up(d_in, kMxPad) / kMxBlock : round_up(d_in, kQBlock) / kQBlock;
+    const RowSpan out = RowSpan::matrix(y, T, d_out * eb, ldy, eb);
+    if (shares_memory(out, RowSpan::matrix(x.codes, T, col_x, x.ld, 1)) || shares_memory(out, RowSpan::matrix(x.scales, T, col_xs, x.lds, 1)) ||
+        shares_memory(out, RowSpan::matrix(w.codes, rows_w, col_w, w.ld, 1)) ||
+        shares_memory(out, RowSpan::matrix(w.scales, rows_w, round_up(d_in, kMxPad) / kMxBlock, w.lds, 1)) ||
+        shares_memory(out, RowSpan::array(seg.offsets, ((int64_t)num_experts + 1) * 4)))
+        return LORA_ERR_INVALID_ARG;
     MxParams p = product_params(xa.bits, x, T, d_in, w, d_out, y, ldy, accumulate);
     p.offsets = seg.offsets;
     p.experts = num_experts;

@@ -14,6 +14,7 @@
 //   3. seg_scatter one workgroup per chunk: perm[pos] = row, plus the tile
 //                  records the shrink / expand / backward kernels walk.
 #include "device_common.h"
+#include "host_checks.h"
 
 namespace lora {
 
@@ -705,6 +706,8 @@ extern "C" int lora_expert_segments(const int32_t* expert_ids, int32_t T, int32_
     const int rc = seg_check(expert_ids, rows, num_experts, seg, ws, ws_bytes);
     if (rc != LORA_OK || T == 0) return rc;
     if (!pos || ((uintptr_t)pos & 3u)) return LORA_ERR_INVALID_ARG;
+    // (the choices are read again after places have been written)
+    if (shares_memory(RowSpan::array(pos, (int64_t)rows * 4), RowSpan::array(expert_ids, (int64_t)rows * 4))) return LORA_ERR_INVALID_ARG;
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (rows <= kExpertSmallRows && num_experts <= kSmallMaxA) {
         SegSmallJobs jobs{};

@@ -639,7 +639,9 @@ int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int
  * rows are by adapter; the rows that go through the experts lie sorted, expert e's
  * at seg.offsets[e] .. seg.offsets[e + 1] - 1.  Adapters of the sorted rows are
  * applied as of any rows (lora_segments_build over the sorted rows' adapter ids).
- * No output of these calls shares memory with an input unless a call says so.
+ * No output of these calls shares memory with an input or another output unless a call
+ * says so (LORA_ERR_INVALID_ARG; rows of one may lie between the rows of the other, as
+ * columns of a wider matrix do).
  */
 
 /*
@@ -682,8 +684,8 @@ int lora_expert_combine(int dtype, const void* o, int64_t ldo, int32_t T, int32_
  * sum over d of dy[t] o[pos[t k + j]] (fp32, a fixed order; 0 for a choice without a
  * place).  dy [T, lddy], o [T k, ldo], d_o [T k, lddo] (dtype); dw [T k] fp32.  Rows
  * of d_o that no choice names are left as they are; d_o may be NULL, and dw may be
- * (then o is not read and may be too).  d_o may be o itself: a row is read before it
- * is written.  One kernel.
+ * (then o is not read and may be too).  d_o may be o itself, with its pitch: a row is
+ * read before it is written.  One kernel.
  */
 int lora_expert_combine_backward(int dtype, const void* dy, int64_t lddy, const void* o, int64_t ldo, int32_t T, int32_t d, int32_t k,
                                  const int32_t* pos, const float* w, void* d_o, int64_t lddo, float* dw, void* stream);
