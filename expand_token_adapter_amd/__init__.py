@@ -998,25 +998,36 @@ def lora_expert_combine(o: torch.Tensor, w: torch.Tensor, seg: ExpertSegments, y
     return y
 
 
-def lora_expert_combine_backward(dy: torch.Tensor, o: torch.Tensor, w: torch.Tensor, seg: ExpertSegments,
-                                 d_o: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None):
+def lora_expert_combine_backward(dy: torch.Tensor, o: Optional[torch.Tensor], w: torch.Tensor, seg: ExpertSegments,
+                                 d_o: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, *,
+                                 need_d_o: bool = True, need_dw: bool = True):
     """The combine's gradient: d_o[pos[t, j]] = w[t, j] dy[t] and dw[t, j] = <dy[t], o[pos[t, j]]> (float32; 0 for a
     choice of no expert).  Returns (d_o, dw).  Rows of d_o behind the last expert's are left as they are (zeros in a
-    new d_o); d_o may be o."""
+    new d_o); d_o may be o.  One of them that is not needed is not computed (None); without dw, o is not read and may be
+    None."""
     fn = "lora_expert_combine_backward"
     _expert_segments(fn, seg)
+    if not need_d_o and not need_dw or (d_o is not None and not need_d_o) or (dw is not None and not need_dw):
+        raise ValueError(f"{fn}: one gradient at least is computed, and none that is not needed is passed")
     pdy, d, lddy, code = _matrix(fn, dy, "dy", seg.tokens, seg.index)
-    po, d1, ldo, c1 = _matrix(fn, o, "o", seg.T, seg.index)
-    _same(fn, "o", d1, c1, d, code)
+    po = ldo = pd = ldd = pdw = 0
+    if o is not None:
+        po, d1, ldo, c1 = _matrix(fn, o, "o", seg.T, seg.index)
+        _same(fn, "o", d1, c1, d, code)
+    elif need_dw:
+        raise ValueError(f"{fn}: dw needs o")
     pw = _router_weights(fn, seg, w)
-    if d_o is None:
-        d_o = torch.zeros(seg.T, d, dtype=dy.dtype, device=dy.device)
-    if dw is None:
-        dw = torch.empty(seg.tokens, seg.k, dtype=torch.float32, device=dy.device)
-    pd, d2, ldd, c2 = _matrix(fn, d_o, "d_o", seg.T, seg.index)
-    _same(fn, "d_o", d2, c2, d, code, pd, pdy)
+    if need_d_o:
+        if d_o is None:
+            d_o = torch.zeros(seg.T, d, dtype=dy.dtype, device=dy.device)
+        pd, d2, ldd, c2 = _matrix(fn, d_o, "d_o", seg.T, seg.index)
+        _same(fn, "d_o", d2, c2, d, code, pd, pdy)
+    if need_dw:
+        if dw is None:
+            dw = torch.empty(seg.tokens, seg.k, dtype=torch.float32, device=dy.device)
+        pdw = _router_weights(fn, seg, dw, "dw")
     st = _launch_on(seg.index, _abi.load().lora_expert_combine_backward, code, pdy, lddy, po, ldo, seg.tokens, d, seg.k,
-                    seg.pos.data_ptr(), pw, pd, ldd, _router_weights(fn, seg, dw, "dw"))
+                    seg.pos.data_ptr(), pw, pd, ldd, pdw)
     if st:
         _abi.check(fn, st)
     return d_o, dw
