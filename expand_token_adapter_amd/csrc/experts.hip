@@ -223,13 +223,20 @@ int launch_combine(int dtype, const ExpertParams& p, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
+// Waves that take a token of the combine's gradient (the kernel has the figures), and
+// workgroups for all of them.
+int backward_waves(int32_t T, int32_t d) { return T < 1024 || d >= 2048 ? 4 : 1; }
+int64_t backward_grid(int32_t T, int32_t d) {
+    const int per = kThreads / kWave / backward_waves(T, d);
+    return ((int64_t)T + per - 1) / per;
+}
 template <int DT>
 void launch_backward(const ExpertParams& p, hipStream_t st) {
-    const dim3 block(kThreads);
-    if (p.T < 1024 || p.d >= 2048)
-        hipLaunchKernelGGL((expert_combine_backward_kernel<DT, 4>), dim3((unsigned)p.T), block, 0, st, p);
+    const dim3 grid((unsigned)backward_grid(p.T, p.d)), block(kThreads);
+    if (backward_waves(p.T, p.d) == 4)
+        hipLaunchKernelGGL((expert_combine_backward_kernel<DT, 4>), grid, block, 0, st, p);
     else
-        hipLaunchKernelGGL((expert_combine_backward_kernel<DT, 1>), dim3((unsigned)((p.T + 3) / 4)), block, 0, st, p);
+        hipLaunchKernelGGL((expert_combine_backward_kernel<DT, 1>), grid, block, 0, st, p);
 }
 
 }  // namespace
@@ -313,7 +320,7 @@ extern "C" int lora_expert_combine_backward(int dtype, const void* dy, int64_t l
     if (rc == LORA_OK && dw) rc = check_matrix(o, d, ldo);
     if (rc == LORA_OK && d_o) rc = check_matrix(d_o, d, lddo);
     if (rc != LORA_OK) return rc;
-    if (!grid_fits(T, kThreads)) return LORA_ERR_UNSUPPORTED;
+    if (!grid_fits(backward_grid(T, d), kThreads)) return LORA_ERR_UNSUPPORTED;
     const RowSpan in_dy = rows_span(dtype, dy, T, d, lddy), in_o = rows_span(dtype, o, (int64_t)T * k, d, ldo);
     const RowSpan in_w = choices_span(w, T, k), in_pos = choices_span(pos, T, k);
     const RowSpan out_o = rows_span(dtype, d_o, (int64_t)T * k, d, lddo), out_w = choices_span(dw, T, k);

@@ -641,7 +641,9 @@ int lora_base_product_mx(int dtype, int32_t x_bits, lora_quant x, int32_t T, int
  * applied as of any rows (lora_segments_build over the sorted rows' adapter ids).
  * No output of these calls shares memory with an input or another output unless a call
  * says so (LORA_ERR_INVALID_ARG; rows of one may lie between the rows of the other, as
- * columns of a wider matrix do).
+ * columns of a wider matrix do).  LORA_ERR_UNSUPPORTED from the calls that move rows for
+ * more than a launch has threads for: more than 2^35 - 2048 values T d; for
+ * lora_expert_combine_backward more than 2^26 - 4 tokens, or 2^24 - 1 where d >= 2048.
  */
 
 /*
