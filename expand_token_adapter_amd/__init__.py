@@ -93,6 +93,9 @@ def _rows(t: torch.Tensor, name: str):
         rows, cols = t.shape
         pitch, step = t.stride()
         if step == 1:
+            # (one row has no pitch: its stride is any number, 1 in a contiguous transpose)
+            if rows == 1 and (pitch < cols or pitch % 8):
+                pitch = cols
             return t.data_ptr(), rows, cols, pitch
     raise ValueError(f"{name} must be 2-D with contiguous rows")
 
@@ -782,7 +785,8 @@ def _matrix(fn: str, t: torch.Tensor, name: str, rows: int, index: int):
     shape, stride = t.shape, t.stride()
     code = _DTYPES.get(t.dtype)
     if len(shape) == 2 and stride[1] == 1 and shape[0] == rows and t.get_device() == index and code is not None:
-        return t.data_ptr(), shape[1], stride[0], code
+        # (one row has no pitch: its stride is any number, 1 in a contiguous transpose)
+        return t.data_ptr(), shape[1], stride[0] if rows > 1 else shape[1], code
     _on_gpu(t)
     _dtype_code(t)
     _rows(t, name)
