@@ -87,10 +87,18 @@ def _on_gpu(*ts: Optional[torch.Tensor]) -> None:
             raise ValueError("tensors must be on the GPU")
 
 
+def _fits(name: str, *sizes: int) -> None:
+    """ValueError for a size that the C calls' int32 would take as another number."""
+    if max(sizes) > 2 ** 31 - 1:
+        raise ValueError(f"{name}: sizes are at most 2^31 - 1, got {max(sizes)}")
+
+
 def _rows(t: torch.Tensor, name: str):
     """(pointer, rows, cols, pitch) of a 2-D tensor whose rows are contiguous."""
     if t.dim() == 2:
         rows, cols = t.shape
+        if (rows | cols) >> 31:
+            _fits(name, rows, cols)
         pitch, step = t.stride()
         if step == 1:
             # (one row has no pitch: its stride is any number, 1 in a contiguous transpose)
@@ -255,6 +263,7 @@ class _Quant:
         _on_gpu(codes, scales)
         if codes.device != scales.device:
             raise ValueError("codes and scales must live on one device")
+        _fits("an 8-bit matrix", rows, cols)
         block = _abi.LORA_QUANT_BLOCK
         for name, t, r, c, unit in (("codes", codes, rows, -(-cols // block) * block, block),
                                     ("scales", scales, scale_rows, -(-cols // (4 * block)) * 4, 4)):
@@ -321,6 +330,7 @@ class _Mx:
         _on_gpu(codes, scales)
         if codes.device != scales.device:
             raise ValueError("codes and scales must live on one device")
+        _fits("a 4-bit matrix", rows, cols)
         pad = -(-cols // _abi.LORA_MX_PAD) * _abi.LORA_MX_PAD
         for name, t, c, unit in (("codes", codes, pad // 2, _abi.LORA_MX_PAD // 2),
                                  ("scales", scales, pad // _abi.LORA_MX_BLOCK, _abi.LORA_MX_PAD // _abi.LORA_MX_BLOCK)):
@@ -387,6 +397,7 @@ class Segments:
 
     def __init__(self, T: int, num_adapters: int, device: torch.device):
         lib = _abi.load()
+        _fits("rows grouped by adapter", T, num_adapters)
         self.T = T
         self.num_adapters = num_adapters
         i32 = dict(dtype=torch.int32, device=device)
@@ -415,6 +426,7 @@ class ExpertSegments(Segments):
         # segments; every part begins at 16 bytes)
         lib = _abi.load()
         T = tokens * k
+        _fits("choices of experts", tokens, k, T, num_experts)
         elems = [num_experts, num_experts + 1, max(T, 1), 1, max(1, lib.lora_segments_sched_elems(T, num_experts)), T]
         parts = torch.zeros(sum((n + 3) // 4 * 4 for n in elems), dtype=torch.int32, device=device).split(
             [m for n in elems for m in (n, -n % 4)])
@@ -785,6 +797,8 @@ def _matrix(fn: str, t: torch.Tensor, name: str, rows: int, index: int):
     shape, stride = t.shape, t.stride()
     code = _DTYPES.get(t.dtype)
     if len(shape) == 2 and stride[1] == 1 and shape[0] == rows and t.get_device() == index and code is not None:
+        if (shape[0] | shape[1]) >> 31:
+            _fits(f"{fn}: {name}", *shape)
         # (one row has no pitch: its stride is any number, 1 in a contiguous transpose)
         return t.data_ptr(), shape[1], stride[0] if rows > 1 else shape[1], code
     _on_gpu(t)
