@@ -9,7 +9,7 @@ extern "C" int lora_abi_version(void) { return LORA_ABI_VERSION; }
 extern "C" const char* lora_status_string(int status) {
     switch (status) {
         case LORA_OK: return "ok";
-        case LORA_ERR_INVALID_ARG: return "invalid argument (null pointer, size, pitch, alignment or enum)";
+        case LORA_ERR_INVALID_ARG: return "invalid argument (null pointer, size, pitch, alignment, enum or shared memory)";
         case LORA_ERR_UNSUPPORTED: return "unsupported shape (row lengths and pitches must be multiples of 8)";
         case LORA_ERR_WORKSPACE: return "workspace missing or too small";
         case LORA_ERR_HIP: return "HIP launch failed";

@@ -92,7 +92,9 @@ constexpr int mx_waves(int kind, int bits, int dtype) {
 // split), and for the small kernels 900 and 500 more and 400 products of up to 64 rows: on
 // those that the numbers were not fitted to, the choice is 0.4% slower than the best in the
 // mean (few rows 0.6%; experts' products, whose rows are spread as the router likes, 2.4%;
-// without the 64 x 32 tile 3.6% and experts' 7.7%).
+// without the 64 x 32 tile 3.6% and experts' 7.7%).  The times rank choices; those of the
+// largest products are too low (6783 x 4096 x 14336 158 us for 216, from 8-bit rows with
+// products cut 223 for 282, in halves 488 for 578).
 inline float mx_time(int kind, int bits, int dtype, int64_t tiles, int32_t steps, int32_t s, float outputs) {
     const MxTile& c = kMxTiles[kind];
     const int f = bits == 4 ? 0 : dtype == LORA_BF16 ? 1 : 2;

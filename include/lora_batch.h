@@ -80,7 +80,7 @@ extern "C" {
 /* Status codes returned by every entry point. */
 enum {
     LORA_OK = 0,
-    LORA_ERR_INVALID_ARG = -1, /* bad pointer, size, pitch or enum */
+    LORA_ERR_INVALID_ARG = -1, /* bad pointer, size, pitch or enum, or memory that may not be shared */
     LORA_ERR_UNSUPPORTED = -2, /* valid but outside what the kernels cover */
     LORA_ERR_WORKSPACE = -3,   /* workspace missing or too small */
     LORA_ERR_HIP = -4,         /* a HIP launch failed */
