@@ -325,7 +325,7 @@ extern "C" int lora_expert_combine_backward(int dtype, const void* dy, int64_t l
     const RowSpan in_w = choices_span(w, T, k), in_pos = choices_span(pos, T, k);
     const RowSpan out_o = rows_span(dtype, d_o, (int64_t)T * k, d, lddo), out_w = choices_span(dw, T, k);
     // (rows in place are read before they are written, if they are the same rows)
-    const bool in_place = d_o == o && lddo == ldo;
+    const bool in_place = d_o == o && (lddo == ldo || (int64_t)T * k == 1);
     if (d_o && (shares_memory(out_o, in_dy) || shares_memory(out_o, in_w) || shares_memory(out_o, in_pos) ||
                 (dw && !in_place && shares_memory(out_o, in_o)) || (dw && shares_memory(out_o, out_w))))
         return LORA_ERR_INVALID_ARG;

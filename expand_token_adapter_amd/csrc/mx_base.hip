@@ -97,7 +97,8 @@ int check_product(int dtype, int32_t bits, const lora_quant& x, int32_t T, int32
     return LORA_OK;
 }
 bool valid_product(int dtype, MxRowsArg x, int32_t T, int32_t d_in, int32_t d_out, int32_t accumulate) {
-    return valid_dtype(dtype) && (x.bits == 4 || x.bits == 8) && (!x.cut || (x.bits == 8 && dtype == LORA_BF16)) && T >= 0 && d_in >= 1 && d_out >= 1 && (accumulate == 0 || accumulate == 1);
+    const bool rows = x.bits == 4 ? !x.cut : x.bits == 8 && (!x.cut || dtype == LORA_BF16);
+    return valid_dtype(dtype) && rows && T >= 0 && d_in >= 1 && d_out >= 1 && (accumulate == 0 || accumulate == 1);
 }
 MxParams product_params(int32_t bits, const lora_quant& x, int32_t T, int32_t d_in, const lora_quant& w, int32_t d_out, void* y,
                         int64_t ldy, int32_t accumulate) {

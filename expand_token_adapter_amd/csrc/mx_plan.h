@@ -1,8 +1,8 @@
 // mx_plan.h -- which kernel, tile and split of k a product with a 4-bit weight takes,
 // and the LDS of a tile (host and device, no HIP).
 //
-// Measured (us, bf16 y, 4-bit rows / 8-bit rows with products cut; rows x k x outputs; the last two kernels read
-// the weight straight into registers):
+// Measured (us, bf16 y, 4-bit rows / 8-bit rows with products cut; rows x k x outputs; the
+// last two kernels read the weight straight into registers):
 //                          64x32      64x64     128x128    256x128    256x256    16x16      32x16
 //     1 x  4096 x  4096  5.4/6.9    6.4/7.9                                    3.4/3.7    4.6/4.8
 //    16 x 14336 x  4096   13/19      15/20                                     9.7/12.8    13/16

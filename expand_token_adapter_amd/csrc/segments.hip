@@ -468,8 +468,9 @@ __global__ __launch_bounds__(kScanThreads) void seg_small_kernel(SegSmallJobs jo
 //      build does.  The first one writes the totals.
 // m grows with the number of choices so that there are at most kExpertChunks chunks.
 // Up to kExpertSmallRows choices take the one-workgroup build (us, it against these two
-// kernels, calls in a row; behind other work the two take 1.5 to 2 more): 2048 of 8 experts 4.8 against 7.7, 4096 of 8 6.8 / 7.8 and of 300 10.2 / 10.0,
-// 8192 of 8 10.7 / 8.0, 13566 18.4 / 8.1, 54264 of 64 88 / 9.6.
+// kernels, calls in a row; behind other work the two take 1.5 to 2 more): 2048 of 8
+// experts 4.8 against 7.7, 4096 of 8 6.8 / 7.8 and of 300 10.2 / 10.0, 8192 of 8 10.7 / 8.0,
+// 13566 18.4 / 8.1, 54264 of 64 88 / 9.6.
 constexpr int kExpertChunks = 256;
 constexpr int kExpertSmallRows = 4096;
 

@@ -41,6 +41,19 @@ def test_columns_of_one_buffer(dtype):
     assert torch.equal(part(1, T), dy)
 
 
+def test_one_row_in_place_has_no_pitch():
+    """The C call with one choice: its row over itself, whatever the pitches say."""
+    from expand_token_adapter_amd import _abi
+
+    seg = lb.lora_expert_segments(torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 1)
+    dy, o, w, dw = torch.randn(1, D, device="cuda"), torch.randn(1, D, device="cuda"), torch.rand(1, 1, device="cuda"), torch.zeros(1, 1, device="cuda")
+    want = lb.lora_expert_combine_backward(dy, o, w, seg)
+    st = torch.cuda.current_stream().cuda_stream
+    assert _abi.load().lora_expert_combine_backward(_abi.LORA_F32, dy.data_ptr(), D, o.data_ptr(), D + 8, 1, D, 1, seg.pos.data_ptr(), w.data_ptr(),
+                                                    o.data_ptr(), D, dw.data_ptr(), st) == _abi.LORA_OK
+    assert torch.equal(o, want[0]) and torch.equal(dw, want[1])
+
+
 def test_overlapping_rows_are_refused():
     seg = _seg()
     w = torch.rand(T, K, device="cuda")
